@@ -64,11 +64,13 @@ const char* const kClassNames[kNumClasses] = {"moba_centroids", "moba_gate", "mo
                                                "moba_bwd_dkdv", "moba_bwd_dq", "moba_bwd_aux"};
 
 // Brackets one kernel launch: an NVTX range named for its class (seen by profilers; a no-op
-// otherwise) and, when timing is enabled, CUDA events on the launching stream.
+// otherwise) and, when timing is enabled, CUDA events on the launching stream. A launch outside
+// the timed classes (cls < 0) brings its own name and is counted only.
 struct Scope {
   int cls; cudaStream_t s; cudaEvent_t a = nullptr, b = nullptr; bool on = false;
-  Scope(int c, cudaStream_t st) : cls(c), s(st) {
-    nvtxRangePushA(kClassNames[c]);
+  Scope(int c, cudaStream_t st, const char* name = nullptr) : cls(c), s(st) {
+    nvtxRangePushA(name ? name : kClassNames[c]);
+    if (cls < 0) return;
     Timing& T = timing();
     std::lock_guard<std::mutex> g(T.mu);
     if (T.enabled) { on = true; a = T.get(); b = T.get(); cudaEventRecord(a, s); }
@@ -225,9 +227,10 @@ cudaError_t run_gate(const void* q, const float* cents, const int32_t* cu_dev,
   return launch_gate(q, cents, cu_dev, nseq, max_nb, T, H, G, d, B, topk, idx, s);
 }
 
-#define MOBA_LAUNCH(cls, stream, expr)                      \
+#define MOBA_LAUNCH(cls, stream, expr) MOBA_LAUNCH_NAMED(cls, nullptr, stream, expr)
+#define MOBA_LAUNCH_NAMED(cls, name, stream, expr)          \
   do {                                                      \
-    Scope _sc((cls), (stream));                             \
+    Scope _sc((cls), (stream), (name));                     \
     cudaError_t _e = (expr);                                \
     _sc.done();                                             \
     if (_e != cudaSuccess) return MOBA_ERR_CUDA;            \
@@ -766,6 +769,270 @@ unsigned long long moba_set_wait_limit_ns(unsigned long long ns) {
 }
 
 int moba_set_diag_stall(int on) { return g_diag_stall.exchange(on != 0 ? 1 : 0); }
+
+// ------------------------------------------------------------------ norm + rotary position
+namespace {
+
+int check_norm(const void* q, long long q_ld, const void* k, long long k_ld, const float* wq,
+               const float* wk, const float* rope, int n_pos, int rot, const int32_t* pos, int T,
+               int Hq, int Hkv, int d, float eps, int interleaved) {
+  if (T < 0 || Hq < 1 || Hkv < 1 || n_pos < 1) return MOBA_ERR_ARG;
+  if (d != 64 && d != 128) return MOBA_ERR_UNSUPPORTED;
+  if (Hq > 65536 || Hkv > 65536) return MOBA_ERR_UNSUPPORTED;
+  // the grid has one warp per token and chunk of up to 16 heads
+  if (static_cast<long long>(T) * (static_cast<long long>(Hq) + Hkv) >= (1LL << 33))
+    return MOBA_ERR_UNSUPPORTED;
+  if (rot < 16 || rot > d || rot % 16 != 0) return MOBA_ERR_UNSUPPORTED;
+  if (q_ld < static_cast<long long>(Hq) * d || k_ld < static_cast<long long>(Hkv) * d ||
+      q_ld % 8 != 0 || k_ld % 8 != 0)
+    return MOBA_ERR_ARG;
+  if (!(eps >= 0.f) || eps > 1e30f || (interleaved != 0 && interleaved != 1)) return MOBA_ERR_ARG;
+  if (T == 0) return MOBA_OK;
+  if (!q || !k || !wq || !wk || !rope || !pos) return MOBA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(wq) || !aligned16(wk) || !aligned16(rope) ||
+      (reinterpret_cast<uintptr_t>(pos) & 3u) != 0)
+    return MOBA_ERR_ARG;
+  return MOBA_OK;
+}
+
+NormLaunch norm_launch(const void* q, long long q_ld, const void* k, long long k_ld,
+                       const float* wq, const float* wk, const float* rope, int n_pos, int rot,
+                       const int32_t* pos, int T, int Hq, int Hkv, int d, float eps,
+                       int interleaved) {
+  NormLaunch N{};
+  N.q = q; N.k = k; N.q_ld = q_ld; N.k_ld = k_ld; N.wq = wq; N.wk = wk; N.rope = rope;
+  N.pos = pos; N.T = T; N.Hq = Hq; N.Hkv = Hkv; N.d = d; N.n_pos = n_pos; N.rot = rot;
+  N.adjacent = interleaved != 0; N.eps = eps;
+  return N;
+}
+
+}  // namespace
+
+int moba_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride,
+                      const float* q_weight, const float* k_weight, const float* rope, int n_pos,
+                      int rot_dim, const int32_t* positions, int T, int Hq, int Hkv, int d,
+                      float eps, int interleaved, void* q_out, void* k_out, void* stream) {
+  int st = check_norm(q, q_stride, k, k_stride, q_weight, k_weight, rope, n_pos, rot_dim,
+                      positions, T, Hq, Hkv, d, eps, interleaved);
+  if (st != MOBA_OK || T == 0) return st;
+  if (!q_out || !k_out || !aligned16(q_out) || !aligned16(k_out)) return MOBA_ERR_ARG;
+  if ((st = device_check(nullptr)) != MOBA_OK) return st;
+  NormLaunch N = norm_launch(q, q_stride, k, k_stride, q_weight, k_weight, rope, n_pos, rot_dim,
+                             positions, T, Hq, Hkv, d, eps, interleaved);
+  N.oq = q_out; N.ok = k_out;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MOBA_LAUNCH_NAMED(-1, "moba_qk_norm_rope", s, launch_qk_norm(N, s));
+  return MOBA_OK;
+}
+
+size_t moba_qk_norm_rope_bwd_workspace_bytes(int Hq, int Hkv, int d) {
+  if (Hq < 1 || Hkv < 1 || Hq > 65536 || Hkv > 65536 || (d != 64 && d != 128)) return 0;
+  return up256(static_cast<size_t>(qk_norm_bwd_ctas(Hq, Hkv, d, kNumSms)) * 2 * d * 4);
+}
+
+int moba_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long long k_stride,
+                          const float* q_weight, const float* k_weight, const float* rope,
+                          int n_pos, int rot_dim, const int32_t* positions, const void* d_q_out,
+                          const void* d_k_out, int T, int Hq, int Hkv, int d, float eps,
+                          int interleaved, void* dq, void* dk, float* d_q_weight,
+                          float* d_k_weight, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  int st = check_norm(q, q_stride, k, k_stride, q_weight, k_weight, rope, n_pos, rot_dim,
+                      positions, T, Hq, Hkv, d, eps, interleaved);
+  if (st != MOBA_OK) return st;
+  if (!d_q_weight || !d_k_weight || !aligned16(d_q_weight) || !aligned16(d_k_weight) ||
+      !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return MOBA_ERR_ARG;
+  if (T > 0 && (!d_q_out || !d_k_out || !dq || !dk || !aligned16(d_q_out) ||
+                !aligned16(d_k_out) || !aligned16(dq) || !aligned16(dk)))
+    return MOBA_ERR_ARG;
+  if (workspace_bytes < moba_qk_norm_rope_bwd_workspace_bytes(Hq, Hkv, d))
+    return MOBA_ERR_WORKSPACE;
+  if ((st = device_check(nullptr)) != MOBA_OK) return st;
+  NormLaunch N = norm_launch(q, q_stride, k, k_stride, q_weight, k_weight, rope, n_pos, rot_dim,
+                             positions, T, Hq, Hkv, d, eps, interleaved);
+  N.dyq = d_q_out; N.dyk = d_k_out; N.oq = dq; N.ok = dk;
+  N.part = static_cast<float*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // no rows: the weights' gradients are zero (a sum over no CTA)
+  const int ctas = T > 0 ? qk_norm_bwd_ctas(Hq, Hkv, d, kNumSms) : 0;
+  if (T > 0)
+    MOBA_LAUNCH_NAMED(-1, "moba_qk_norm_rope_bwd", s, launch_qk_norm_bwd(N, ctas, s));
+  MOBA_LAUNCH_NAMED(-1, "moba_qk_norm_dw", s,
+                    launch_qk_norm_dw(N.part, ctas, d, d_q_weight, d_k_weight, s));
+  return MOBA_OK;
+}
+
+// ---------------------------------------------------------------------------- paged cache
+namespace {
+
+int check_cache(const moba_paged_cache* c, PagedCache* P) {
+  if (!c) return MOBA_ERR_ARG;
+  if (c->nseq < 1 || c->nseq > 65535 || c->max_pages < 1 || c->num_pages < 1 || c->Hkv < 1)
+    return MOBA_ERR_ARG;
+  if (c->dtype != MOBA_CACHE_BF16 && c->dtype != MOBA_CACHE_E4M3) return MOBA_ERR_ARG;
+  if (c->d != 64 && c->d != 128) return MOBA_ERR_UNSUPPORTED;
+  if (c->Hkv > 1024) return MOBA_ERR_UNSUPPORTED;
+  int lg = 4;
+  while (lg < 12 && (1 << lg) != c->page_size) ++lg;
+  if ((1 << lg) != c->page_size) return MOBA_ERR_UNSUPPORTED;  // a power of two, 16 .. 4096
+  if ((static_cast<long long>(c->max_pages) << lg) > (1LL << 30)) return MOBA_ERR_UNSUPPORTED;
+  const bool fp8 = c->dtype == MOBA_CACHE_E4M3;
+  if (!c->k || !c->v || !c->page_table || !c->seq_lens || !aligned16(c->k) || !aligned16(c->v))
+    return MOBA_ERR_ARG;
+  if (fp8 != (c->k_scale != nullptr) || fp8 != (c->v_scale != nullptr)) return MOBA_ERR_ARG;
+  if (fp8 && (!aligned16(c->k_scale) || !aligned16(c->v_scale))) return MOBA_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(c->page_table) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(c->seq_lens) & 3u) != 0)
+    return MOBA_ERR_ARG;
+  if (c->block_sums) {
+    if (!aligned16(c->block_sums) || c->block_size < 1) return MOBA_ERR_ARG;
+    if (c->block_size % 64 != 0 || c->block_size % c->page_size != 0 ||
+        c->block_size > (1 << 24))
+      return MOBA_ERR_UNSUPPORTED;
+  }
+  P->k = c->k; P->v = c->v;
+  P->k_scale = static_cast<uint8_t*>(c->k_scale);
+  P->v_scale = static_cast<uint8_t*>(c->v_scale);
+  P->sums = c->block_sums;
+  P->page_table = c->page_table; P->seq_lens = c->seq_lens;
+  P->nseq = c->nseq; P->max_pages = c->max_pages; P->num_pages = c->num_pages;
+  P->page_log = lg; P->G = c->Hkv; P->d = c->d; P->B = c->block_sums ? c->block_size : 0;
+  P->fp8 = fp8;
+  return MOBA_OK;
+}
+
+struct PagedLayout { size_t seg_first, seg_count, part_o, part_ml, seg_tiles, entries, keys,
+                     marks, total; };
+
+PagedLayout paged_layout(const PagedShape& S, int d, int topk) {
+  PagedLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o = up256(o + bytes); return at; };
+  const size_t nseg = static_cast<size_t>(S.nseg);
+  const size_t rows = static_cast<size_t>(S.slots) * S.rows_per_tile;
+  L.seg_first = take(nseg * 4);
+  L.seg_count = take(nseg * 4);
+  L.part_o = take(rows * d * 4);
+  L.part_ml = take(rows * 8);
+  L.seg_tiles = take(topk ? nseg * 4 : 0);
+  L.entries = take(topk ? nseg * S.ent_cap * 8 : 0);
+  const bool global = topk && S.gate_global;
+  L.keys = take(global ? nseg * S.rows_per_tile * S.nb_cap * 8 : 0);
+  L.marks = take(global ? nseg * S.nb_cap * 4 : 0);
+  L.total = o;
+  return L;
+}
+
+// topk = 0: dense.
+int paged_plan(const moba_paged_cache* c, int Hq, int rows, int topk, PagedCache* P,
+               PagedShape* S) {
+  int st = check_cache(c, P);
+  if (st != MOBA_OK) return st;
+  if (Hq < 1 || Hq % P->G != 0 || rows < 1 || topk < 0) return MOBA_ERR_ARG;
+  if (Hq / P->G > 256 || rows > 256 || topk > kMaxTopk) return MOBA_ERR_UNSUPPORTED;
+  if (topk && !P->sums) return MOBA_ERR_ARG;
+  *S = paged_shape(*P, rows, Hq, topk, kNumSms);
+  if (S->nseg >= (1LL << 24) ||
+      static_cast<long long>(P->nseq) * rows * Hq >= (1LL << 31) / 64)
+    return MOBA_ERR_UNSUPPORTED;
+  if (topk && S->nb_cap > kMaxBlocksPerSeq) return MOBA_ERR_UNSUPPORTED;
+  return MOBA_OK;
+}
+
+int paged_run(const moba_paged_cache* c, const void* q, int Hq, int rows, int topk, float scale,
+              int32_t* idx, void* o, float* lse, void* workspace, size_t workspace_bytes,
+              void* stream) {
+  PagedLaunch D{};
+  int st = paged_plan(c, Hq, rows, topk, &D.cache, &D.shape);
+  if (st != MOBA_OK) return st;
+  if (!(scale > 0.f) || scale > 1e30f) return MOBA_ERR_ARG;
+  if (!q || !o || !lse || !workspace || !aligned16(q) || !aligned16(o) || !aligned16(lse) ||
+      (idx && !aligned16(idx)) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return MOBA_ERR_ARG;
+  const PagedLayout L = paged_layout(D.shape, c->d, topk);
+  if (workspace_bytes < L.total) return MOBA_ERR_WORKSPACE;
+  if ((st = device_check(nullptr)) != MOBA_OK) return st;
+  D.q = q; D.rows = rows; D.Hq = Hq; D.topk = topk; D.scale = scale;
+  D.seg_first = at<int>(workspace, L.seg_first);
+  D.seg_count = at<int>(workspace, L.seg_count);
+  D.part_o = at<float>(workspace, L.part_o);
+  D.part_ml = at<float>(workspace, L.part_ml);
+  D.seg_tiles = at<int>(workspace, L.seg_tiles);
+  D.entries = at<int>(workspace, L.entries);
+  D.keys = at<unsigned long long>(workspace, L.keys);
+  D.marks = at<unsigned int>(workspace, L.marks);
+  D.idx = idx; D.o = o; D.lse = lse;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (topk) MOBA_LAUNCH_NAMED(kDecode, "moba_paged_gate", s, launch_paged_gate(D, s));
+  MOBA_LAUNCH_NAMED(kDecode, "moba_paged_attn", s, launch_paged_attn(D, s));
+  MOBA_LAUNCH_NAMED(kDecode, "moba_paged_merge", s, launch_paged_merge(D, s));
+  return MOBA_OK;
+}
+
+}  // namespace
+
+int moba_cache_append(const moba_paged_cache* cache, const void* k, long long k_stride,
+                      const void* v, long long v_stride, const int32_t* cu_seqlens_q_dev, int Tq,
+                      void* stream) {
+  PagedCache P{};
+  int st = check_cache(cache, &P);
+  if (st != MOBA_OK) return st;
+  const long long row = static_cast<long long>(P.G) * P.d;
+  if (Tq < 0 || k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return MOBA_ERR_ARG;
+  if (Tq >= (1 << 30)) return MOBA_ERR_UNSUPPORTED;
+  if (Tq == 0) return MOBA_OK;
+  if (!k || !v || !cu_seqlens_q_dev || !aligned16(k) || !aligned16(v) ||
+      (reinterpret_cast<uintptr_t>(cu_seqlens_q_dev) & 3u) != 0)
+    return MOBA_ERR_ARG;
+  if ((st = device_check(nullptr)) != MOBA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MOBA_LAUNCH_NAMED(-1, "moba_cache_append", s,
+                    launch_cache_append(P, k, v, k_stride, v_stride, cu_seqlens_q_dev, Tq,
+                                        kNumSms, s));
+  return MOBA_OK;
+}
+
+int moba_cache_read(const moba_paged_cache* cache, const int32_t* cu_seqlens_dev, int T, void* k,
+                    void* v, void* stream) {
+  PagedCache P{};
+  int st = check_cache(cache, &P);
+  if (st != MOBA_OK) return st;
+  if (T < 0) return MOBA_ERR_ARG;
+  if (T >= (1 << 30)) return MOBA_ERR_UNSUPPORTED;
+  if (T == 0) return MOBA_OK;
+  if (!k || !v || !cu_seqlens_dev || !aligned16(k) || !aligned16(v) ||
+      (reinterpret_cast<uintptr_t>(cu_seqlens_dev) & 3u) != 0)
+    return MOBA_ERR_ARG;
+  if ((st = device_check(nullptr)) != MOBA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MOBA_LAUNCH_NAMED(-1, "moba_cache_read", s, launch_cache_read(P, k, v, cu_seqlens_dev, T, s));
+  return MOBA_OK;
+}
+
+size_t moba_paged_workspace_bytes(const moba_paged_cache* cache, int Hq, int rows_per_seq,
+                                  int topk) {
+  PagedCache P{};
+  PagedShape S;
+  if (paged_plan(cache, Hq, rows_per_seq, topk, &P, &S) != MOBA_OK) return 0;
+  return paged_layout(S, P.d, topk).total;
+}
+
+int moba_paged_attn_fwd(const moba_paged_cache* cache, const void* q, int Hq, int rows_per_seq,
+                        float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  return paged_run(cache, q, Hq, rows_per_seq, 0, scale, nullptr, o, lse, workspace,
+                   workspace_bytes, stream);
+}
+
+int moba_paged_decode_fwd(const moba_paged_cache* cache, const void* q, int Hq, int rows_per_seq,
+                          int topk, float scale, int32_t* block_idx_out, void* o, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (topk < 1) return MOBA_ERR_ARG;
+  return paged_run(cache, q, Hq, rows_per_seq, topk, scale, block_idx_out, o, lse, workspace,
+                   workspace_bytes, stream);
+}
 
 int moba_timing_enable(int enable) {
   Timing& T = timing();

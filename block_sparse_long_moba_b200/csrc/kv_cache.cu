@@ -1,0 +1,376 @@
+// A paged key-value cache: new rows written into their pages (rounded to 8 bits when the cache is
+// e4m3), the key sum of every MoBA block kept as its rows arrive, and the cached rows read back
+// packed.
+//
+// Pool layout: k, v [num_pages, Hkv, page_size, d], so that the rows of one page and kv head are
+// contiguous (what the attention over them reads). Token u of sequence s lives in page
+// page_table[s, u / page_size], slot u % page_size.
+// e4m3 rows carry one power-of-two scale, stored as its biased exponent byte b (the value is
+// code * 2^(b - 127)): the smallest 2^(b - 127) >= 2^-126 that keeps the row's largest magnitude
+// within 448. e4m3 has its own exponent, so a power of two costs at most one binade of its range
+// against amax / 448 and none of its 3 mantissa bits; scaling by it is exact, so a code is the
+// value rounded once (to nearest even), and code * scale is exact in bf16.
+// The sum of block j of a sequence lives at the block's first page, sums [num_pages, Hkv, d] fp32,
+// of the keys as given (before the rounding to 8 bits), which the gate scores; the mean differs by
+// the factor 1 / block_size, common to all blocks that it ranks.
+//
+// Bound: HBM (each row read once, written once). One cluster per (sequence, block that the call
+// touches, group of kv heads) walks the block's new rows; d / 8 lanes hold one head's row, so the
+// row maximum is a 3- or 4-step butterfly. The CTAs of a cluster take consecutive parts of the
+// rows and rank 0 adds their column sums in rank order through distributed shared memory: no
+// atomics, the same sum every time.
+#include <cooperative_groups.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace cg = cooperative_groups;
+
+namespace moba {
+
+namespace {
+
+constexpr int kCacheThreads = 256;
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(w[e] << 16);
+    x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+  }
+}
+
+// Scale byte of a row whose largest magnitude is amax (448 = 1.75 * 2^8).
+__device__ __forceinline__ int scale_byte(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int b = static_cast<int>(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(b, 1);
+}
+
+__device__ __forceinline__ uint2 to_e4m3(const float (&x)[8], int b) {
+  const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+        make_float2(x[4 * h] * inv, x[4 * h + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+        make_float2(x[4 * h + 2] * inv, x[4 * h + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    w[h] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+struct CacheView {
+  uint8_t *k, *v, *ks, *vs;
+  float* sums;
+  const int32_t *page_table, *seq_lens;
+  int nseq, max_pages, num_pages, page_log, G, B;
+};
+
+struct AppendArgs {
+  CacheView C;
+  const __nv_bfloat16 *k, *v;
+  long long k_ld, v_ld;
+  const int32_t* cuq;
+  int Tq, heads;  // heads: kv heads per CTA
+};
+
+// First unit of sequence s: a sequence with n new rows touches at most n / B + 2 blocks, and
+// cuq[s] / B + 2 s leaves room for that without a scan over the sequences before it.
+__device__ __forceinline__ int first_unit(int cuq_s, int s, int B) { return cuq_s / B + 2 * s; }
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const AppendArgs A) {
+  constexpr int LPR = D / 8;               // lanes per row
+  constexpr int SLOTS = kCacheThreads / LPR;
+  constexpr int U = 4;                     // rows in flight per lane group
+  __shared__ float red[SLOTS][D];          // column sums per slot, then per head in red[head]
+  const CacheView& C = A.C;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int CS = static_cast<int>(cluster.num_blocks());
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int unit = blockIdx.x / CS;
+  int lo = 0, hi = C.nseq;  // largest s with first_unit(s) <= unit
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first_unit(__ldg(A.cuq + mid), mid, C.B) <= unit) lo = mid; else hi = mid;
+  }
+  const int s = lo, c0 = __ldg(A.cuq + s), c1 = __ldg(A.cuq + s + 1);
+  const int L = __ldg(C.seq_lens + s);
+  // host and device copies may disagree: rows outside the buffers are never touched
+  const int n = (c0 >= 0 && c1 >= c0 && c1 <= A.Tq) ? c1 - c0 : 0;
+  const int p0 = max(L - n, 0);  // first new position
+  const int b = p0 / C.B + unit - first_unit(c0, s, C.B);
+  const int cap = static_cast<int>(
+      min(static_cast<long long>(C.max_pages) << C.page_log, 0x7fffffffll));
+  const int u0 = max(static_cast<int>(min(static_cast<long long>(b) * C.B, 0x7fffffffll)), p0);
+  const int u1 = static_cast<int>(min(static_cast<long long>(b + 1) * C.B,
+                                      static_cast<long long>(min(L, cap))));
+  if (u1 <= u0) return;  // the whole cluster
+  const int32_t* pages = C.page_table + static_cast<size_t>(s) * C.max_pages;
+  const int per = (u1 - u0 + CS - 1) / CS;
+  const int a0 = u0 + rank * per, a1 = min(u1, a0 + per);
+  const int g0 = blockIdx.y * A.heads, nh = min(A.heads, C.G - g0);
+  const int slot = threadIdx.x / LPR, l = threadIdx.x % LPR;
+  const int TP = SLOTS / A.heads;  // rows per pass
+  const int hh = slot % A.heads, tt = slot / A.heads;
+  const bool mine = hh < nh && tt < TP;
+  const int g = g0 + hh;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  const int mask = (1 << C.page_log) - 1;
+  for (int u = a0; u < a1; u += U * TP) {  // uniform over the CTA: shuffles below
+    uint4 kr[U], vr[U];
+    int pid[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int x = u + i * TP + tt;
+      const bool in = mine && x < a1;
+      const long long row = c0 + (x - (L - n));
+      kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+      pid[i] = -1;
+      if (in) {
+        kr[i] = __ldcs(reinterpret_cast<const uint4*>(A.k + row * A.k_ld + g * D) + l);
+        vr[i] = __ldcs(reinterpret_cast<const uint4*>(A.v + row * A.v_ld + g * D) + l);
+        pid[i] = __ldg(pages + (x >> C.page_log));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int x = u + i * TP + tt;
+      const bool ok = pid[i] >= 0 && pid[i] < C.num_pages;  // false when the row is not ours
+      const size_t at = ((static_cast<size_t>(ok ? pid[i] : 0) * C.G + g) << C.page_log) +
+                        (x & mask);
+      float kx[8], vx[8];
+      unpack8(kr[i], kx);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += kx[e];
+      if (FP8) {
+        unpack8(vr[i], vx);
+        float ka = 0.f, va = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          ka = fmaxf(ka, fabsf(kx[e]));
+          va = fmaxf(va, fabsf(vx[e]));
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) {
+          ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
+          va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
+        }
+        const int kb = scale_byte(ka), vb = scale_byte(va);
+        if (ok) {
+          *reinterpret_cast<uint2*>(C.k + at * D + l * 8) = to_e4m3(kx, kb);
+          *reinterpret_cast<uint2*>(C.v + at * D + l * 8) = to_e4m3(vx, vb);
+          if (l == 0) {
+            C.ks[at] = static_cast<uint8_t>(kb);
+            C.vs[at] = static_cast<uint8_t>(vb);
+          }
+        }
+      } else if (ok) {
+        *reinterpret_cast<uint4*>(C.k + (at * D + l * 8) * 2) = kr[i];
+        *reinterpret_cast<uint4*>(C.v + (at * D + l * 8) * 2) = vr[i];
+      }
+    }
+  }
+  if (!C.sums) return;  // uniform over the grid
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[slot][l * 8 + e] = mine ? sum[e] : 0.f;
+  __syncthreads();
+  // red[h] <- sum over the row slots of head h, slots in order
+  for (int x = threadIdx.x; x < nh * D; x += kCacheThreads) {
+    const int h = x / D, col = x % D;
+    float f = red[h][col];
+    for (int i = 1; i < TP; ++i) f += red[i * A.heads + h][col];
+    red[h][col] = f;
+  }
+  cluster.sync();
+  if (rank == 0) {
+    const int home = __ldg(pages + ((static_cast<long long>(b) * C.B) >> C.page_log));
+    if (home >= 0 && home < C.num_pages) {
+      const bool fresh = static_cast<long long>(b) * C.B >= p0;  // the block begins with new rows
+      for (int x = threadIdx.x; x < nh * D; x += kCacheThreads) {
+        float* dst = C.sums + (static_cast<size_t>(home) * C.G + g0) * D + x;
+        float f = fresh ? 0.f : *dst;
+        for (int r = 0; r < CS; ++r) f += *cluster.map_shared_rank(&red[x / D][x % D], r);
+        *dst = f;
+      }
+    }
+  }
+  cluster.sync();  // peers' shared memory stays until rank 0 has read it
+}
+
+struct ReadArgs {
+  CacheView C;
+  __nv_bfloat16 *k, *v;  // [T, G, D]
+  const int32_t* cu;
+  int T;
+};
+
+// kReadRows consecutive packed rows per CTA; thread t < kReadRows finds row t's sequence, page and
+// slot, then d / 8 lanes copy one head's row.
+constexpr int kReadRows = 32;
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const ReadArgs A) {
+  constexpr int LPR = D / 8, SLOTS = kCacheThreads / LPR, U = 4;
+  __shared__ long long at[kReadRows];  // (page * G) << page_log plus slot; -1: zeros, -2: NaN
+  const CacheView& C = A.C;
+  const int r0 = blockIdx.x * kReadRows;
+  const int nr = min(kReadRows, A.T - r0);
+  if (threadIdx.x < nr) {
+    const int r = r0 + threadIdx.x;
+    int lo = 0, hi = C.nseq;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(A.cu + mid) <= r) lo = mid; else hi = mid;
+    }
+    const long long u = static_cast<long long>(r) - __ldg(A.cu + lo);
+    long long x = -1;
+    if (u >= 0 && u < __ldg(C.seq_lens + lo) && r < __ldg(A.cu + lo + 1)) {
+      x = -2;
+      if ((u >> C.page_log) < C.max_pages) {
+        const int pid = __ldg(C.page_table + static_cast<size_t>(lo) * C.max_pages +
+                              (u >> C.page_log));
+        if (pid >= 0 && pid < C.num_pages)
+          x = ((static_cast<long long>(pid) * C.G) << C.page_log) +
+              (u & ((1 << C.page_log) - 1));
+      }
+    }
+    at[threadIdx.x] = x;
+  }
+  __syncthreads();
+  const int slot = threadIdx.x / LPR, l = threadIdx.x % LPR;
+  const int total = nr * C.G;  // (row, head) pairs, heads fastest
+  for (int x0 = slot; x0 < total; x0 += U * SLOTS) {
+    uint4 kr[U], vr[U];
+    float kf[U], vf[U];
+    long long base[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int x = x0 + i * SLOTS;
+      base[i] = -1;
+      kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+      kf[i] = vf[i] = 0.f;
+      if (x < total) {
+        base[i] = at[x / C.G];
+        if (base[i] >= 0) {
+          const size_t row = static_cast<size_t>(base[i]) +
+                             (static_cast<size_t>(x % C.G) << C.page_log);
+          if (FP8) {
+            const uint2 a = __ldcs(reinterpret_cast<const uint2*>(C.k + row * D) + l);
+            const uint2 b = __ldcs(reinterpret_cast<const uint2*>(C.v + row * D) + l);
+            kr[i].x = a.x; kr[i].y = a.y;
+            vr[i].x = b.x; vr[i].y = b.y;
+            kf[i] = __uint_as_float(static_cast<uint32_t>(__ldg(C.ks + row)) << 23);
+            vf[i] = __uint_as_float(static_cast<uint32_t>(__ldg(C.vs + row)) << 23);
+          } else {
+            kr[i] = __ldcs(reinterpret_cast<const uint4*>(C.k + row * D * 2) + l);
+            vr[i] = __ldcs(reinterpret_cast<const uint4*>(C.v + row * D * 2) + l);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int x = x0 + i * SLOTS;
+      if (x >= total) break;
+      auto widen = [&](uint4 u, float f) {
+        if (base[i] == -2) return make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        if (!FP8) return u;
+        uint32_t w[4];
+        const uint32_t c[2] = {u.x, u.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+              static_cast<__nv_fp8x2_storage_t>(c[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
+          const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          const __nv_bfloat162 r = __floats2bfloat162_rn(p.x * f, p.y * f);
+          w[e] = *reinterpret_cast<const uint32_t*>(&r);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      };
+      const size_t dst = (static_cast<size_t>(r0) * C.G + x) * D + l * 8;
+      __stcs(reinterpret_cast<uint4*>(A.k + dst), widen(kr[i], kf[i]));
+      __stcs(reinterpret_cast<uint4*>(A.v + dst), widen(vr[i], vf[i]));
+    }
+  }
+}
+
+CacheView view_of(const PagedCache& P) {
+  CacheView C;
+  C.k = static_cast<uint8_t*>(P.k); C.v = static_cast<uint8_t*>(P.v);
+  C.ks = P.k_scale; C.vs = P.v_scale; C.sums = P.sums;
+  C.page_table = P.page_table; C.seq_lens = P.seq_lens;
+  C.nseq = P.nseq; C.max_pages = P.max_pages; C.num_pages = P.num_pages;
+  C.page_log = P.page_log; C.G = P.G; C.B = P.B;
+  return C;
+}
+
+template <int D, bool FP8>
+cudaError_t append(const PagedCache& P, AppendArgs A, int sms, cudaStream_t s) {
+  constexpr int SLOTS = kCacheThreads / (D / 8);
+  // Without block sums the block size only cuts the work.
+  if (!A.C.sums) A.C.B = 1024;
+  const int B = A.C.B;
+  const long long units = A.Tq / B + 2ll * P.nseq;
+  // Rows a touched block brings on average, cut so that a CTA keeps at least 64 of them.
+  const long long rows = std::min<long long>(B, std::max<long long>(1, A.Tq / P.nseq));
+  int cs = 1;
+  while (cs < 8 && rows / (2 * cs) >= 64) cs *= 2;
+  // As many kv heads per CTA as fit its threads (their rows are neighbours in the input), fewer
+  // while the grid would not fill the SMs a few times.
+  int heads = std::min(P.G, SLOTS);
+  const long long busy = std::max<long long>(1, A.Tq / B + P.nseq) * cs;
+  while (heads > 1 && busy * ((P.G + heads - 1) / heads) < 4ll * sms) heads = (heads + 1) / 2;
+  A.heads = heads;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * cs), (P.G + heads - 1) / heads);
+  cfg.blockDim = dim3(kCacheThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(cs);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_append_kernel<D, FP8>, A);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const PagedCache& P, const void* k, const void* v, long long k_ld,
+                                long long v_ld, const int32_t* cuq, int Tq, int sms,
+                                cudaStream_t s) {
+  AppendArgs A{};
+  A.C = view_of(P);
+  A.k = static_cast<const __nv_bfloat16*>(k);
+  A.v = static_cast<const __nv_bfloat16*>(v);
+  A.k_ld = k_ld; A.v_ld = v_ld; A.cuq = cuq; A.Tq = Tq;
+  if (P.d == 64) return P.fp8 ? append<64, true>(P, A, sms, s) : append<64, false>(P, A, sms, s);
+  return P.fp8 ? append<128, true>(P, A, sms, s) : append<128, false>(P, A, sms, s);
+}
+
+cudaError_t launch_cache_read(const PagedCache& P, void* k, void* v, const int32_t* cu, int T,
+                              cudaStream_t s) {
+  ReadArgs A{};
+  A.C = view_of(P);
+  A.k = static_cast<__nv_bfloat16*>(k);
+  A.v = static_cast<__nv_bfloat16*>(v);
+  A.cu = cu; A.T = T;
+  const unsigned grid = (T + kReadRows - 1) / kReadRows;
+  if (P.d == 64) {
+    if (P.fp8) cache_read_kernel<64, true><<<grid, kCacheThreads, 0, s>>>(A);
+    else cache_read_kernel<64, false><<<grid, kCacheThreads, 0, s>>>(A);
+  } else {
+    if (P.fp8) cache_read_kernel<128, true><<<grid, kCacheThreads, 0, s>>>(A);
+    else cache_read_kernel<128, false><<<grid, kCacheThreads, 0, s>>>(A);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace moba

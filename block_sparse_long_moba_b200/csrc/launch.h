@@ -164,6 +164,72 @@ cudaError_t launch_bwd_dkdv(const BwdLaunch& L, cudaStream_t stream);
 cudaError_t launch_bwd_dq(const BwdLaunch& L, cudaStream_t stream);
 cudaError_t launch_bwd_finish(const BwdLaunch& L, cudaStream_t stream);
 
+// SMs of a B200: sizes the grids and workspaces below without a device query.
+constexpr int kNumSms = 148;
+
+// Norm + rotary position of q and k, and its gradients (csrc/qk_norm.cu).
+struct NormLaunch {
+  const void *q, *k;          // bf16 [T, Hq, d] and [T, Hkv, d], tokens q_ld / k_ld elements apart
+  const void *dyq, *dyk;      // backward: gradients of the outputs, packed
+  long long q_ld, k_ld;
+  const float *wq, *wk;       // [d]
+  const float* rope;          // [n_pos, rot]: cosines, then sines
+  const int32_t* pos;         // [T]
+  void *oq, *ok;              // outputs (dq, dk in the backward pass), packed
+  float* part;                // backward: [CTAs][2][d]
+  int T, Hq, Hkv, d, n_pos, rot;
+  bool adjacent;
+  float eps;
+};
+cudaError_t launch_qk_norm(const NormLaunch& L, cudaStream_t s);
+int qk_norm_bwd_ctas(int Hq, int Hkv, int d, int sms);
+cudaError_t launch_qk_norm_bwd(const NormLaunch& L, int ctas, cudaStream_t s);
+cudaError_t launch_qk_norm_dw(const float* part, int n, int d, float* dwq, float* dwk,
+                              cudaStream_t s);
+
+// Paged key-value cache (csrc/kv_cache.cu) and attention over it (csrc/paged.cu).
+struct PagedCache {
+  void *k, *v;                 // [num_pages, G, page_size, d] bf16 or e4m3
+  uint8_t *k_scale, *v_scale;  // e4m3: [num_pages, G, page_size] biased exponents
+  float* sums;                 // nullable [num_pages, G, d]
+  const int32_t* page_table;   // [nseq, max_pages]
+  const int32_t* seq_lens;     // [nseq]
+  int nseq, max_pages, num_pages, page_log, G, d, B;
+  bool fp8;
+};
+cudaError_t launch_cache_append(const PagedCache& P, const void* k, const void* v, long long k_ld,
+                                long long v_ld, const int32_t* cuq, int Tq, int sms,
+                                cudaStream_t s);
+cudaError_t launch_cache_read(const PagedCache& P, void* k, void* v, const int32_t* cu, int T,
+                              cudaStream_t s);
+
+struct PagedShape {
+  int rows_per_tile, nrt;  // rows of a segment (8 or 16), row tiles per (sequence, kv head)
+  long long nseg, slots;   // segments, partial results
+  int ctas;                // of the attention kernel
+  int nb_cap, ent_cap;     // blocks of a full sequence, selected blocks of a segment at most
+  int gate_ctas;           // CTAs of one segment's gate
+  bool gate_global;        // keys and marks of the gate in the workspace
+};
+PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms);
+struct PagedLaunch {
+  PagedCache cache;
+  PagedShape shape;
+  const void* q;  // bf16 [nseq * rows, Hq, d]
+  int rows, Hq, topk;  // topk 0: dense
+  float scale;
+  int *seg_first, *seg_count, *seg_tiles, *entries;
+  float *part_o, *part_ml;
+  unsigned long long* keys;
+  unsigned int* marks;
+  int32_t* idx;
+  void* o;
+  float* lse;
+};
+cudaError_t launch_paged_gate(const PagedLaunch& L, cudaStream_t s);
+cudaError_t launch_paged_attn(const PagedLaunch& L, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedLaunch& L, cudaStream_t s);
+
 // Whole forward pass on a caller-provided workspace (the body of moba_attn_fwd); the partial
 // outputs of one query chunk are kept under `partial_budget` bytes.
 int attn_fwd_impl(const void* q, const void* k, const void* v, const int32_t* cu_dev,

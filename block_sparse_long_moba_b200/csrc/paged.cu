@@ -1,0 +1,1185 @@
+// Attention of the newest rows of cached sequences over a paged key-value cache: over every cached
+// key (dense), or over the blocks that the MoBA gate selects. Pages and scales as in kv_cache.cu.
+//
+// A segment is (sequence s, kv head g, row tile): up to kRows = 8 NT of the rows_per_seq * (Hq/Hkv)
+// rows that share kv head g. Its keys are cut into tiles of 8 KB of K and 8 KB of V. The tiles of
+// all segments form one line, split evenly over the warps of a grid of one CTA per SM, so one
+// long sequence, many short ones and a ragged batch all load every SM alike (the host need not
+// know the lengths). Each warp is on its own: it streams its tiles through a private ring in
+// shared memory (16-byte cp.async, two tiles ahead of the one in work, across segment borders)
+// and keeps the running maximum and sum of the softmax in registers. A segment that one warp has
+// whole is written at once; otherwise each of its warps leaves a normalised fp32 partial with its
+// (max, sum), and paged_merge_kernel joins them in warp order.
+//
+// Products on mma.sync m16n8k16 with the KEYS as the 16-row operand: S^T = K Q^T (16 keys x 8
+// rows), O^T = V^T P^T (16 columns of d x 8 rows). A decode step has 1 to 16 rows per kv head, so
+// the 128-row tile of tcgen05.mma would be 1/8 full at best; here a row tile of 8 wastes at most
+// 7 rows, and the tensor pipe stays far below the memory time: 16 cached bf16 rows of K and V at
+// d = 128 are 8 KB = ~350 clocks of one SM's share of HBM against 16 mma of 16 clocks on each of
+// four tensor units. Bound: HBM, each selected key and value row once.
+//
+// e4m3 caches: codes widen exactly to f16, products run in f16 with fp32 accumulation. q is bf16
+// and becomes f16 exactly after a power-of-two scaling of its row (elements 2^-25 below the row's
+// largest round to zero); a key's scale multiplies its logit in fp32; a value's scale goes into
+// the weight p relative to the largest scale seen, by powers of two. p is kept at 2^15 times its
+// value, so that weights down to 2^-29 of the largest stay normal f16 numbers.
+// Rounding: p to bf16 (e4m3 cache: f16) for the second product; logits, maxima, sums (of the
+// unrounded p) and outputs are fp32 until the final bf16.
+#include <algorithm>
+#include <cfloat>
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "sm100.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace moba {
+
+namespace {
+
+constexpr int kPagedWarps = 4;
+constexpr int kPagedThreads = kPagedWarps * 32;
+constexpr int kStages = 3;
+constexpr int kTileBytes = 8192;  // of K, and of V, per stage
+
+// ------------------------------------------------------------------------------ PTX wrappers
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0 bytes read: the destination is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two e4m3 codes (low 16 bits) -> two f16, exact
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+  uint32_t r;
+  asm("{\n .reg .b16 lo;\n cvt.u16.u32 lo, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}"
+      : "=r"(r)
+      : "r"(codes));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The kernel before this one on the stream may still run (programmatic launch): wait for its
+// results before the first read of them; let the next kernel's CTAs be scheduled early.
+__device__ __forceinline__ void wait_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void allow_next_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------------- arguments
+struct PagedArgs {
+  const __nv_bfloat16* q;  // [nseq * rows, Hq, D]
+  const uint8_t *k, *v, *ks, *vs;
+  const float* sums;
+  const int32_t *page_table, *seq_lens;
+  int nseq, max_pages, num_pages, page_log, G, B;
+  int rows, Hq, group, nrt, nseg;  // nrt row tiles per (sequence, kv head); nseg segments
+  int topk, nb_cap, ent_cap, tiles_per_block;
+  float scale_log2;
+  // workspace
+  int* seg_first;        // [nseg] first worker of a split segment
+  int* seg_count;        // [nseg] its workers; 1: written directly
+  float* part_o;         // [slots][kRows][D]
+  float2* part_ml;       // [slots][kRows]
+  int* seg_tiles;        // sparse: [nseg] tiles, -1: a page outside the pool
+  int2* entries;         // sparse: [nseg][ent_cap] (block, rows that selected it)
+  unsigned long long* keys;  // sparse: [nseg][kRows][nb_cap] order keys (large caches)
+  unsigned int* marks;       // sparse: [nseg][nb_cap] rows that selected a block (large caches)
+  int32_t* idx;          // sparse, nullable: [Hq, nseq * rows, topk]
+  __nv_bfloat16* o;
+  float* lse;
+};
+
+struct Seg { int s, g, rt; };
+__device__ __forceinline__ Seg seg_of(const PagedArgs& A, int seg) {
+  Seg x;
+  x.rt = seg % A.nrt;
+  const int sg = seg / A.nrt;
+  x.g = sg % A.G;
+  x.s = sg / A.G;
+  return x;
+}
+
+// Cached tokens of sequence s, cut to what its row of the page table can hold (a longer sequence
+// is reported as bad by the callers).
+__device__ __forceinline__ int seq_len(const PagedArgs& A, int s, bool* over) {
+  const int L = max(__ldg(A.seq_lens + s), 0);
+  const long long cap = static_cast<long long>(A.max_pages) << A.page_log;
+  *over = L > cap;
+  return static_cast<int>(min(static_cast<long long>(L), cap));
+}
+
+// ------------------------------------------------------------------------------------- layout
+// Byte offset of 16-byte piece c of row r in a tile of rows of RB bytes. Eight consecutive rows'
+// pieces c fall into eight different 16-byte columns of the 128-byte bank line (ldmatrix reads
+// them without conflicts).
+template <int RB>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  if (RB == 64) return static_cast<uint32_t>(r) * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  return static_cast<uint32_t>(r) * RB + ((c ^ (r & 7)) << 4);
+}
+
+template <int D, bool FP8>
+struct Tile {
+  static constexpr int RB = D * (FP8 ? 1 : 2);  // bytes of a row
+  static constexpr int KT = kTileBytes / RB;    // keys: 32, 64 or 128
+  static constexpr int kScaleBytes = FP8 ? 2 * KT : 0;
+  static constexpr int kStage = 2 * kTileBytes + kScaleBytes;
+  static constexpr int kWarpBytes = kStages * kStage;
+};
+
+// ------------------------------------------------------------------------------ attention
+// Worker w of n takes tiles [w U / n, (w + 1) U / n).
+__device__ __forceinline__ long long range_start(long long U, int w, int n) {
+  return U * w / n;
+}
+
+template <int D, bool FP8, int NT, bool SPARSE>
+__global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const PagedArgs A) {
+  using TL = Tile<D, FP8>;
+  constexpr int RB = TL::RB, KT = TL::KT, kRows = 8 * NT, CPR = RB / 16;
+  constexpr int KS = D / 16;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ long long prefix[kPagedThreads + 1];
+  __shared__ int4 ring[kPagedWarps][4];  // tiles in flight: segment, first key, keys | flags, rows
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = lane & 3, n4 = lane >> 2;
+  allow_next_kernel();
+  if (SPARSE) wait_previous_kernel();
+
+  // Tiles of one segment.
+  auto tiles_of = [&](int seg) -> int {
+    if (SPARSE) return max(A.seg_tiles[seg], 0);
+    bool over;
+    return (seq_len(A, seg / (A.G * A.nrt), &over) + KT - 1) / KT;
+  };
+  // Prefix sums: thread t owns a run of segments.
+  const int per = (A.nseg + kPagedThreads - 1) / kPagedThreads;
+  {
+    long long mine = 0;
+    const int a = min(A.nseg, tid * per), b = min(A.nseg, a + per);
+    for (int i = a; i < b; ++i) mine += tiles_of(i);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) prefix[warp] = incl;
+    __syncthreads();
+    long long before = 0, all = 0;
+    for (int w = 0; w < kPagedWarps; ++w) {
+      const long long x = prefix[w];
+      if (w < warp) before += x;
+      all += x;
+    }
+    __syncthreads();
+    prefix[tid] = before + incl - mine;
+    if (tid == 0) prefix[kPagedThreads] = all;
+    __syncthreads();
+  }
+  const long long U = prefix[kPagedThreads];
+  // Neighbouring workers sit on different SMs, so that few tiles still use many of them.
+  const int workers = static_cast<int>(
+      min(static_cast<long long>(gridDim.x) * kPagedWarps, U));
+  const int me = warp * gridDim.x + blockIdx.x;
+  if (me >= workers) return;  // no block-wide barrier below
+  const long long ub = range_start(U, me, workers), ue = range_start(U, me + 1, workers);
+
+  // Segment of tile ub: the run that holds it, then 32 segments at a time.
+  int seg0 = 0;
+  long long seg_begin = 0;
+  {
+    int run = 0;
+    for (int x = lane; x < kPagedThreads; x += 32)
+      if (prefix[x] <= ub) run = x;  // ascending in x per lane
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) run = max(run, __shfl_xor_sync(0xffffffffu, run, o));
+    long long at = prefix[run];
+    const int last = min(A.nseg, (run + 1) * per);
+    for (int i = run * per; i < last; i += 32) {
+      const int cnt = i + lane < last ? tiles_of(i + lane) : 0;
+      long long incl = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, at + incl > ub);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        seg0 = i + src;
+        seg_begin = at + __shfl_sync(0xffffffffu, incl - cnt, src);
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+
+  uint8_t* wbase = smem + warp * TL::kWarpBytes;
+  const uint32_t wsm = smem_u32(wbase);
+
+  // ---- loader: walks the tiles ahead of the consumer
+  int l_seg = seg0, l_tile = static_cast<int>(ub - seg_begin), l_tiles = tiles_of(seg0);
+  long long l_left = ue - ub;
+  Seg l_id = seg_of(A, seg0);
+  bool l_over;
+  int l_len = seq_len(A, l_id.s, &l_over);
+  int4 pend = make_int4(-1, 0, 0, 0);  // tile whose page ids are in my_pid
+  int pend_g = 0, my_pid = -1;
+  auto look_up = [&]() {  // next tile's place and pages
+    pend.x = -1;
+    if (l_left == 0) return;
+    while (l_tile >= l_tiles) {
+      if (++l_seg >= A.nseg) {  // lengths changed under the call: nothing more to copy
+        l_left = 0;
+        return;
+      }
+      l_tile = 0;
+      l_tiles = tiles_of(l_seg);
+      if (l_tiles) {
+        l_id = seg_of(A, l_seg);
+        l_len = seq_len(A, l_id.s, &l_over);
+      }
+    }
+    int kpos = l_tile * KT, end = l_len;
+    unsigned rows = 0xffffffffu;
+    if (SPARSE) {
+      const int e = l_tile / A.tiles_per_block;
+      const int2 ent = A.entries[static_cast<size_t>(l_seg) * A.ent_cap + e];
+      kpos = ent.x * A.B + (l_tile - e * A.tiles_per_block) * KT;
+      end = static_cast<int>(min(static_cast<long long>(end),
+                                 (static_cast<long long>(ent.x) + 1) * A.B));
+      rows = static_cast<unsigned>(ent.y);
+    }
+    const int nk = min(KT, end - kpos);
+    my_pid = 0;
+    bool bad = l_over;
+    if (lane < KT / 16 && lane * 16 < nk) {
+      my_pid = __ldg(A.page_table + static_cast<size_t>(l_id.s) * A.max_pages +
+                     ((kpos + lane * 16) >> A.page_log));
+      if (my_pid < 0 || my_pid >= A.num_pages) {
+        bad = true;
+        my_pid = -1;
+      }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    pend = make_int4(l_seg, kpos, nk | (bad ? 1 << 16 : 0), static_cast<int>(rows));
+    pend_g = l_id.g;
+    ++l_tile;
+    --l_left;
+  };
+  auto issue = [&](int stage, int slot4) {  // copies of the pending tile into `stage`
+    if (pend.x >= 0) {
+      if (lane == 0) ring[warp][slot4] = pend;
+      const int nk = pend.z & 0xffff, mask = (1 << A.page_log) - 1;
+      const uint32_t kd = wsm + stage * TL::kStage, vd = kd + kTileBytes;
+#pragma unroll
+      for (int gq = 0; gq < KT / 16; ++gq) {  // 16 keys of one page
+        const int pid = __shfl_sync(0xffffffffu, my_pid, gq);
+        const size_t row0 =
+            ((static_cast<size_t>(max(pid, 0)) * A.G + pend_g) << A.page_log) +
+            ((pend.y + gq * 16) & mask);
+        constexpr int kPerLane = 16 * CPR / 32;  // 16-byte pieces of 16 rows per lane
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          const int piece = i * 32 + lane, r = piece / CPR, cc = piece % CPR;
+          const bool ok = pid >= 0 && gq * 16 + r < nk;
+          const size_t off = (row0 + r) * RB + cc * 16;
+          const uint32_t d = swz<RB>(gq * 16 + r, cc);
+          cp_async16(kd + d, A.k + (ok ? off : 0), ok);
+          cp_async16(vd + d, A.v + (ok ? off : 0), ok);
+        }
+        if (FP8 && lane < 2) {  // 16 scale bytes of K (lane 0) and V (lane 1)
+          const bool ok = pid >= 0 && gq * 16 < nk;
+          cp_async16(vd + kTileBytes + lane * KT + gq * 16,
+                     (lane ? A.vs : A.ks) + (ok ? row0 : 0), ok);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+
+  const int ntiles = static_cast<int>(ue - ub);
+  look_up();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    issue(i, i);
+    look_up();
+  }
+
+  // ---- consumer state
+  int seg = -1, first_tile_of_seg = 0;
+  Seg id{0, 0, 0};
+  uint32_t qf[KS][NT][2];
+  float acc[KS][NT][4];
+  float m[NT][2], l[NT][2], cmul[NT][2];
+  int lim[NT][2];
+  int vref = 0;
+  bool bad = false;
+  long long cur_begin = seg_begin;  // first tile of the current segment on the line
+  int cur_tiles = 0;
+
+  auto begin = [&](int sg) {
+    id = seg_of(A, sg);
+    bool over;
+    const int L = seq_len(A, id.s, &over);
+    bad = over;
+    const int R = A.rows * A.group;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int rr = id.rt * kRows + nt * 8 + n4;  // row whose elements this lane holds
+      const bool in = rr < R;
+      const __nv_bfloat16* src =
+          A.q + (static_cast<size_t>(id.s) * A.rows + (in ? rr / A.group : 0)) * A.Hq * D +
+          (static_cast<size_t>(id.g) * A.group + (in ? rr % A.group : 0)) * D;
+      // the pairs of d that a lane's two B registers hold: 2c and 2c + 8 of each 16 columns, or
+      // 4c and 4c + 2 where the keys' bytes come four to a lane
+      constexpr int kFirst = FP8 ? 4 : 2, kSecond = FP8 ? 2 : 8;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[ks][nt][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + kFirst * c) : 0u;
+        qf[ks][nt][1] =
+            in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + kFirst * c + kSecond) : 0u;
+      }
+      float f = A.scale_log2;
+      if (FP8) {
+        uint32_t top = 0;  // largest magnitude of the row, as bf16 bits
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            top = max(top, max(qf[ks][nt][h] & 0x7fffu, (qf[ks][nt][h] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // times 2^(13 - exponent): the largest element lies in [2^13, 2^14)
+        const int up = min(254, max(1, 267 - static_cast<int>(top >> 7)));
+        const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
+        f *= __uint_as_float(static_cast<uint32_t>(max(254 - up, 1)) << 23);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            qf[ks][nt][h] = pack_f16(__uint_as_float(qf[ks][nt][h] << 16) * mul,
+                                     __uint_as_float(qf[ks][nt][h] & 0xffff0000u) * mul);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        cmul[nt][j] = FP8 ? __shfl_sync(0xffffffffu, f, (2 * c + j) * 4) : f;
+        const int rc = id.rt * kRows + nt * 8 + 2 * c + j;  // row of this lane's result columns
+        lim[nt][j] = rc < R ? L - A.rows + rc / A.group + 1 : 0;  // keys it may see
+        m[nt][j] = -INFINITY;
+        l[nt][j] = 0.f;
+      }
+#pragma unroll
+      for (int ds = 0; ds < KS; ++ds)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[ds][nt][x] = 0.f;
+    }
+    vref = 0;
+  };
+
+  auto finish = [&](int sg, int t0, int t1) {  // this warp had tiles [t0, t1) of the segment
+    const bool whole = t0 == 0 && t1 == cur_tiles;
+    const int R = A.rows * A.group;
+    const size_t slot = static_cast<size_t>(me) + sg;
+    if (t1 == cur_tiles && lane == 0) {
+      int w0 = me;
+      if (!whole) {  // worker of the segment's first tile
+        w0 = static_cast<int>(cur_begin * workers / U);
+        while (range_start(U, w0 + 1, workers) <= cur_begin) ++w0;
+        while (range_start(U, w0, workers) > cur_begin) --w0;
+      }
+      A.seg_first[sg] = w0;
+      A.seg_count[sg] = me - w0 + 1;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float s = l[nt][j];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float nan = __int_as_float(0x7fffffff);
+        float mul = s > 0.f ? 1.f / s : 0.f;
+        if (FP8) mul *= __uint_as_float(static_cast<uint32_t>(max(vref, 1)) << 23);
+        float top = FP8 ? m[nt][j] - 15.f : m[nt][j];
+        if (bad) mul = top = nan;
+        const int col = nt * 8 + 2 * c + j, rr = id.rt * kRows + col;
+        if (rr >= R) continue;
+        if (whole) {
+          const int r = rr / A.group, h = id.g * A.group + rr % A.group;
+          const size_t row = static_cast<size_t>(id.s) * A.rows + r;
+          __nv_bfloat16* dst = A.o + (row * A.Hq + h) * D;
+#pragma unroll
+          for (int ds = 0; ds < KS; ++ds) {
+            const int d0 = ds * 16 + (FP8 ? 2 * n4 : n4), d1 = d0 + (FP8 ? 1 : 8);
+            dst[d0] = __float2bfloat16_rn(acc[ds][nt][j] * mul);
+            dst[d1] = __float2bfloat16_rn(acc[ds][nt][2 + j] * mul);
+          }
+          if (n4 == 0)
+            A.lse[static_cast<size_t>(h) * A.nseq * A.rows + row] =
+                bad ? nan : s > 0.f ? (top + log2f(s)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          float* dst = A.part_o + (slot * kRows + col) * D;
+#pragma unroll
+          for (int ds = 0; ds < KS; ++ds) {
+            const int d0 = ds * 16 + (FP8 ? 2 * n4 : n4), d1 = d0 + (FP8 ? 1 : 8);
+            dst[d0] = acc[ds][nt][j] * mul;
+            dst[d1] = acc[ds][nt][2 + j] * mul;
+          }
+          if (n4 == 0) A.part_ml[slot * kRows + col] = make_float2(top, s);
+        }
+      }
+  };
+
+  // ---- tiles
+  int stage = 0, next_tile = static_cast<int>(ub - seg_begin);
+  for (int it = 0; it < ntiles; ++it) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    const int4 t = ring[warp][it & 3];
+    // the stage that was consumed in the last iteration takes the next tile
+    issue(stage == 0 ? kStages - 1 : stage - 1, (it + kStages - 1) & 3);
+    look_up();
+    if (t.x != seg) {
+      if (seg >= 0) {
+        finish(seg, first_tile_of_seg, cur_tiles);
+        cur_begin += cur_tiles;
+        next_tile = 0;
+      }
+      seg = t.x;
+      cur_tiles = tiles_of(seg);
+      first_tile_of_seg = next_tile;
+      begin(seg);
+    }
+    ++next_tile;
+    const int nk = t.z & 0xffff;
+    bad |= (t.z >> 16) != 0;
+    const unsigned rows = static_cast<unsigned>(t.w);
+    const uint32_t kb = wsm + stage * TL::kStage, vb = kb + kTileBytes;
+    const uint8_t* sc = wbase + stage * TL::kStage + 2 * kTileBytes;
+    int klim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        klim[nt][j] =
+            (!SPARSE || ((rows >> (nt * 8 + 2 * c + j)) & 1)) ? min(lim[nt][j], t.y + nk) : 0;
+#pragma unroll 1
+    for (int sub = 0; sub < KT / 32; ++sub) {
+      if (sub * 32 >= nk) break;
+      float sacc[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sacc[mt][nt][x] = 0.f;
+      // S^T = K Q^T
+      const int krow = sub * 32 + (lane & 15);
+      if (!FP8) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            uint32_t a[4];
+            ldsm4(a, kb + swz<RB>(krow + mt * 16, ks * 2 + (lane >> 4)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<false>(sacc[mt][nt], a, qf[ks][nt][0], qf[ks][nt][1]);
+          }
+      } else {
+#pragma unroll
+        for (int k2 = 0; k2 < KS / 2; ++k2)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            // matrices: (keys 0-7, 16 columns), (keys 8-15, same), then the next 16 columns
+            uint32_t b[4];
+            ldsm4(b, kb + swz<RB>(krow + mt * 16, k2 * 2 + (lane >> 4)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t a[4];
+              a[0] = widen2(b[2 * h]);
+              a[1] = widen2(b[2 * h + 1]);
+              a[2] = widen2(b[2 * h] >> 16);
+              a[3] = widen2(b[2 * h + 1] >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<true>(sacc[mt][nt], a, qf[2 * k2 + h][nt][0], qf[2 * k2 + h][nt][1]);
+            }
+          }
+      }
+      // softmax: this lane holds keys n4 + 8 x of each 16, columns 2c, 2c + 1
+      float kmul[2][2];
+      int vexp[2][2];
+      if (FP8) {
+        int top = 0;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int key = sub * 32 + mt * 16 + x * 8 + n4;
+            kmul[mt][x] = __uint_as_float(static_cast<uint32_t>(sc[key]) << 23);
+            vexp[mt][x] = key < nk ? sc[KT + key] : 0;
+            top = max(top, vexp[mt][x]);
+          }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (top > vref) {  // uniform: a larger value scale than all before
+          const int e = 127 + vref - top;
+          const float f = e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.f;
+#pragma unroll
+          for (int ds = 0; ds < KS; ++ds)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) acc[ds][nt][x] *= f;
+          vref = top;
+        }
+      }
+      float corr[NT][2];
+      bool grew = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float best = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int key = t.y + sub * 32 + mt * 16 + x * 8 + n4;
+              float z = sacc[mt][nt][2 * x + j] * cmul[nt][j];
+              if (FP8) z *= kmul[mt][x];
+              z = key < klim[nt][j] ? z : -INFINITY;
+              sacc[mt][nt][2 * x + j] = z;
+              best = fmaxf(best, z);
+            }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+          const float mn = fmaxf(m[nt][j], best);
+          corr[nt][j] = mn > m[nt][j] ? exp2f(m[nt][j] - mn) : 1.f;  // 0 for the first keys
+          grew |= mn > m[nt][j];
+          m[nt][j] = mn;
+          // no key yet: any finite reference gives p = 0
+          const float ref = (mn == -INFINITY ? 0.f : mn) - (FP8 ? 15.f : 0.f);
+          float sum = 0.f;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float p = exp2f(sacc[mt][nt][2 * x + j] - ref);
+              sacc[mt][nt][2 * x + j] = p;
+              sum += p;
+            }
+          l[nt][j] = fmaf(l[nt][j], corr[nt][j], sum);
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int ds = 0; ds < KS; ++ds)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[ds][nt][x] *= corr[nt][x & 1];
+      }
+      // P^T as the second operand: 8 x 8 pieces turned within the warp
+      uint32_t pf[2][NT][2];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float p0 = sacc[mt][nt][2 * x], p1 = sacc[mt][nt][2 * x + 1];
+            uint32_t u;
+            if (FP8) {
+              const int e = 127 + vexp[mt][x] - vref;
+              const float f = e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.f;
+              u = pack_f16(p0 * f, p1 * f);
+            } else {
+              u = pack_bf16(p0, p1);
+            }
+            pf[mt][nt][x] = transpose8x8(u);
+          }
+      // O^T += V^T P^T
+      if (!FP8) {
+        const int vrow = sub * 32 + ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+#pragma unroll
+        for (int ds = 0; ds < KS; ++ds)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            uint32_t a[4];
+            ldsm4t(a, vb + swz<RB>(vrow + mt * 16, ds * 2 + half));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<false>(acc[ds][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
+          }
+      } else {
+        // matrices: (keys 0-7, 16 columns), (keys 8-15, same), then the next 16 columns; a
+        // register holds columns 2i, 2i + 1 of keys 2c, 2c + 1
+        const int vrow = sub * 32 + (((lane >> 3) & 1) << 3) + (lane & 7);
+#pragma unroll
+        for (int d2 = 0; d2 < KS / 2; ++d2)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            uint32_t b[4];
+            ldsm4t(b, vb + swz<RB>(vrow + mt * 16, d2 * 2 + (lane >> 4)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t lo = __byte_perm(b[2 * h], 0, 0x3120);
+              const uint32_t hi = __byte_perm(b[2 * h + 1], 0, 0x3120);
+              uint32_t a[4];
+              a[0] = widen2(lo);        // column 2i of keys 2c, 2c + 1
+              a[1] = widen2(lo >> 16);  // column 2i + 1
+              a[2] = widen2(hi);        // keys 8 + 2c, 8 + 2c + 1
+              a[3] = widen2(hi >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<true>(acc[2 * d2 + h][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
+            }
+          }
+      }
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+  if (seg >= 0) finish(seg, first_tile_of_seg, next_tile);
+}
+
+// ------------------------------------------------------------------------------------- merge
+// One CTA per (sequence, row, head): the partials of its segment, four warps taking every fourth,
+// joined in a fixed order. Rows without keys get o = 0, lse = -inf; a row whose sequence names a
+// page outside the pool gets NaN.
+template <int D>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs A, int kRows,
+                                                          bool sparse) {
+  __shared__ float sm[4], sl[4], so[4][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int PER = D / 32;
+  const int h = blockIdx.x % A.Hq, row = blockIdx.x / A.Hq;
+  const int s = row / A.rows, r = row % A.rows, g = h / A.group;
+  const int rr = r * A.group + h % A.group, rt = rr / kRows, col = rr % kRows;
+  const int seg = (s * A.G + g) * A.nrt + rt;
+  wait_previous_kernel();
+  bool over;
+  const int L = seq_len(A, s, &over);
+  int count = 0, first = 0;
+  bool bad = over;
+  if (sparse) {
+    const int tiles = A.seg_tiles[seg];
+    bad |= tiles < 0;
+    if (tiles > 0) count = A.seg_count[seg];
+  } else if (L > 0) {
+    count = A.seg_count[seg];
+  }
+  if (count == 1) return;  // written by the warp that had all of it
+  if (count) first = A.seg_first[seg];
+  float m = -INFINITY, l = 0.f, acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  const size_t slot0 = static_cast<size_t>(first) + seg;
+#pragma unroll 4
+  for (int i = warp; i < count; i += 4) {
+    const size_t at = (slot0 + i) * kRows + col;
+    const float2 ml = A.part_ml[at];
+    float o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) {
+      const float2 f = *reinterpret_cast<const float2*>(A.part_o + at * D + lane * PER + e);
+      o[e] = f.x;
+      o[e + 1] = f.y;
+    }
+    if (!(ml.x <= FLT_MAX)) { bad = true; continue; }  // NaN: a bad page
+    if (!(ml.y > 0.f)) continue;
+    const float mn = fmaxf(m, ml.x), a = exp2f(m - mn), b = exp2f(ml.x - mn) * ml.y;
+    l = fmaf(l, a, b);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = fmaf(acc[e], a, b * o[e]);
+    m = mn;
+  }
+  if (lane == 0) {
+    sm[warp] = bad ? __int_as_float(0x7fffffff) : m;
+    sl[warp] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) so[warp][lane * PER + e] = acc[e];
+  __syncthreads();
+  float M = -INFINITY, Lsum = 0.f;
+  bool any_bad = false;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    any_bad |= sm[w] != sm[w];
+    M = fmaxf(M, sm[w]);
+  }
+  float wt[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    wt[w] = sl[w] > 0.f ? exp2f(sm[w] - M) : 0.f;
+    Lsum = fmaf(wt[w], sl[w], Lsum);
+  }
+  const float inv = any_bad ? __int_as_float(0x7fffffff) : Lsum > 0.f ? 1.f / Lsum : 0.f;
+  if (threadIdx.x < D) {
+    float o = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) o = fmaf(wt[w], so[w][threadIdx.x], o);
+    A.o[(static_cast<size_t>(row) * A.Hq + h) * D + threadIdx.x] = __float2bfloat16_rn(o * inv);
+  }
+  if (threadIdx.x == 0)
+    A.lse[static_cast<size_t>(h) * A.nseq * A.rows + row] =
+        any_bad ? __int_as_float(0x7fffffff)
+                : Lsum > 0.f ? (M + log2f(Lsum)) * 0.69314718055994531f : -INFINITY;
+}
+
+// -------------------------------------------------------------------------------------- gate
+// Routing of one segment's rows: scores of the past blocks, the exact top (topk - 1) of each row,
+// and the list of blocks that any of the rows selected, with the rows that did.
+// Scores are q . (block sum): the mean's 1 / B is common to the past blocks, which are all full.
+// They are accumulated in fp64 (products of bf16 and fp32 are exact there), so the selection does
+// not hang on the order of the sum; fp64 runs at half the fp32 rate here and the scores are a
+// small part of the step. One cluster per segment: its CTAs score every CS-th run of 32 blocks
+// (lanes over blocks, the 8 warps over eighths of d, so a sum is widened to fp64 once for all
+// rows), then each row's selection is one warp's: a radix selection on order-preserving 64-bit
+// keys whose 256 bins span only the range still in question (usually two or three sweeps).
+// Equal scores: the lower block first.
+constexpr int kGateThreads = 256;
+constexpr int kGateWarps = kGateThreads / 32;
+
+__device__ __forceinline__ unsigned long long order_key64(double x) {
+  if (x != x) return 0ull;  // NaN: behind every number
+  const unsigned long long u =
+      static_cast<unsigned long long>(__double_as_longlong(x + 0.0));  // -0 -> +0
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+template <int D, int RR>
+__global__ void __launch_bounds__(kGateThreads) paged_gate_kernel(const PagedArgs A, int kRows,
+                                                                  int KT, int in_smem) {
+  constexpr int CP = D + 4;        // padded row of the staged sums
+  constexpr int SL = D / kGateWarps;  // columns of d per warp
+  extern __shared__ __align__(1024) uint8_t smem[];
+  double* qd = reinterpret_cast<double*>(smem);               // [RR][D]
+  double* red = qd + RR * D;                                  // [8][RR][32]
+  float* cs = reinterpret_cast<float*>(red + kGateWarps * RR * 32);  // [32][CP]
+  int* hist = reinterpret_cast<int*>(cs + 32 * CP);           // [8][256]
+  unsigned long long* skeys = reinterpret_cast<unsigned long long*>(hist + kGateWarps * 256);
+  __shared__ int sbad, scan[kGateWarps], stot;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int CS = static_cast<int>(cluster.num_blocks());
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int seg = blockIdx.x / CS;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  allow_next_kernel();
+  const Seg id = seg_of(A, seg);
+  const int R = A.rows * A.group, row0 = id.rt * kRows;
+  const int nrow = min(kRows, R - row0);  // rows of this tile (<= RR)
+  bool over;
+  const int L = seq_len(A, id.s, &over);
+  const int last = L > 0 ? (L - 1) / A.B : -1;  // current block of the newest row
+  unsigned long long* keys =
+      in_smem ? skeys : A.keys + static_cast<size_t>(seg) * kRows * A.nb_cap;
+  unsigned int* marks = in_smem ? reinterpret_cast<unsigned int*>(skeys + RR * A.nb_cap)
+                                : A.marks + static_cast<size_t>(seg) * A.nb_cap;
+  const int32_t* pages = A.page_table + static_cast<size_t>(id.s) * A.max_pages;
+  if (tid == 0) sbad = 0;
+  for (int j = rank * kGateThreads + tid; j <= last; j += CS * kGateThreads) marks[j] = 0;
+  const bool scored = A.topk > 1 && A.topk - 1 < last;
+  if (scored) {
+    for (int x = tid; x < RR * D; x += kGateThreads) {
+      const int rr = row0 + x / D;
+      double v = 0.;
+      if (x / D < nrow)
+        v = static_cast<double>(__bfloat162float(
+            A.q[((static_cast<size_t>(id.s) * A.rows + rr / A.group) * A.Hq +
+                 static_cast<size_t>(id.g) * A.group + rr % A.group) * D + x % D]));
+      qd[x] = v;
+    }
+    for (int j0 = rank * 32; j0 < last; j0 += CS * 32) {
+      __syncthreads();
+      for (int x = tid; x < 32 * (D / 4); x += kGateThreads) {
+        const int j = x / (D / 4), cc = x % (D / 4);
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j0 + j < last) {
+          const int pid =
+              __ldg(pages + ((static_cast<long long>(j0 + j) * A.B) >> A.page_log));
+          if (pid >= 0 && pid < A.num_pages)
+            f = __ldg(reinterpret_cast<const float4*>(
+                          A.sums + (static_cast<size_t>(pid) * A.G + id.g) * D) + cc);
+          else
+            sbad = 1;
+        }
+        *reinterpret_cast<float4*>(cs + j * CP + cc * 4) = f;
+      }
+      __syncthreads();
+      double acc[RR];
+#pragma unroll
+      for (int r = 0; r < RR; ++r) acc[r] = 0.;
+#pragma unroll
+      for (int x = 0; x < SL; x += 4) {
+        const int col = warp * SL + x;
+        const float4 f = *reinterpret_cast<const float4*>(cs + lane * CP + col);
+        const double c[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int r = 0; r < RR; ++r) acc[r] = fma(qd[r * D + col + e], c[e], acc[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < RR; ++r) red[(warp * RR + r) * 32 + lane] = acc[r];
+      __syncthreads();
+      for (int x = tid; x < RR * 32; x += kGateThreads) {
+        const int r = x >> 5, j = j0 + (x & 31);
+        double v = 0.;
+#pragma unroll
+        for (int w = 0; w < kGateWarps; ++w) v += red[(w * RR + r) * 32 + (x & 31)];
+        if (r < nrow && j < last) keys[static_cast<size_t>(r) * A.nb_cap + j] = order_key64(v);
+      }
+    }
+  }
+  cluster.sync();
+  // ---- selection: row r of the tile by warp (r / CS) of rank r % CS
+  for (int r = rank + CS * warp; r < nrow; r += CS * kGateWarps) {
+    const int rr = row0 + r, tok = rr / A.group, h = id.g * A.group + rr % A.group;
+    const int pos = L - A.rows + tok;
+    int32_t* out = A.idx ? A.idx + (static_cast<size_t>(h) * A.nseq * A.rows +
+                                    static_cast<size_t>(id.s) * A.rows + tok) * A.topk
+                         : nullptr;
+    const int i = pos >= 0 ? pos / A.B : -1;  // past blocks, and the current one
+    const int want = min(A.topk - 1, max(i, 0));
+    const unsigned int bit = 1u << r;
+    if (i >= 0 && !over) {
+      const unsigned long long* kr = keys + static_cast<size_t>(r) * A.nb_cap;
+      unsigned long long thr = 0;
+      int need_eq = 0x7fffffff;
+      if (want > 0 && want < i) {
+        unsigned long long base = ~0ull, top = 0;
+#pragma unroll 4
+        for (int j = lane; j < i; j += 32) {
+          base = min(base, kr[j]);
+          top = max(top, kr[j]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          base = min(base, __shfl_xor_sync(0xffffffffu, base, o));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        unsigned long long range = top - base;
+        int w = want;
+        int* hs = hist + warp * 256;
+        while (true) {
+          if (range == 0) {
+            need_eq = w;
+            break;
+          }
+          const int shift = max(0, 56 - __clzll(static_cast<long long>(range)));
+#pragma unroll
+          for (int x = 0; x < 8; ++x) hs[x * 32 + lane] = 0;
+          __syncwarp();
+#pragma unroll 4
+          for (int j = lane; j < i; j += 32) {
+            const unsigned long long d = kr[j] - base;  // wraps above range for smaller keys
+            if (d <= range) atomicAdd(&hs[static_cast<int>(d >> shift)], 1);
+          }
+          __syncwarp();
+          int bins[8], mine = 0;  // lane 0 has the eight highest bins
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            bins[x] = hs[255 - (lane * 8 + x)];
+            mine += bins[x];
+          }
+          int incl = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+          }
+          const int src = __ffs(__ballot_sync(0xffffffffu, incl >= w)) - 1;
+          int above = incl - mine, bin = 0, cnt = 0;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            if (cnt == 0) {
+              if (above + bins[x] >= w) { bin = 255 - (lane * 8 + x); cnt = bins[x]; }
+              else above += bins[x];
+            }
+          bin = __shfl_sync(0xffffffffu, bin, src);
+          cnt = __shfl_sync(0xffffffffu, cnt, src);
+          above = __shfl_sync(0xffffffffu, above, src);
+          w -= above;
+          const unsigned long long step = static_cast<unsigned long long>(bin) << shift;
+          base += step;
+          if (cnt == w) break;  // the whole bin
+          if (shift == 0) {     // one key value: the lowest blocks of it
+            need_eq = w;
+            break;
+          }
+          range = min(range - step, (1ull << shift) - 1);
+          __syncwarp();
+        }
+        thr = base;
+      }
+      int at = 0, eq = 0;
+      if (want > 0)
+        for (int j0 = 0; j0 < i; j0 += 32) {
+          const int j = j0 + lane;
+          const unsigned long long k = want < i && j < i ? kr[j] : 0ull;
+          const bool same = j < i && want < i && k == thr;
+          const unsigned eqs = __ballot_sync(0xffffffffu, same);
+          bool sel = j < i && (want == i || k > thr);
+          if (same) sel = eq + __popc(eqs & ((1u << lane) - 1)) < need_eq;
+          const unsigned sels = __ballot_sync(0xffffffffu, sel);
+          if (sel) {
+            if (out) out[at + __popc(sels & ((1u << lane) - 1))] = j;
+            atomicOr(marks + j, bit);
+          }
+          at += __popc(sels);
+          eq += __popc(eqs);
+        }
+      if (lane == 0) {
+        if (out) out[want] = i;
+        atomicOr(marks + i, bit);
+      }
+    }
+    if (out)
+      for (int x = (i >= 0 && !over ? want + 1 : 0) + lane; x < A.topk; x += 32) out[x] = -1;
+  }
+  cluster.sync();
+  if (rank == 0) {  // the blocks that a row selected, ascending
+    bool bad = over;
+    for (int r = 0; r < CS; ++r) bad |= *cluster.map_shared_rank(&sbad, r) != 0;
+    int2* ent = A.entries + static_cast<size_t>(seg) * A.ent_cap;
+    int total = 0, has_last = 0;
+    for (int j0 = 0; j0 <= last; j0 += kGateThreads) {
+      const int j = j0 + tid;
+      const unsigned int mk = j <= last ? marks[j] : 0u;
+      const unsigned b = __ballot_sync(0xffffffffu, mk != 0);
+      if (lane == 0) scan[warp] = __popc(b);
+      __syncthreads();
+      int before = total, all = 0;
+#pragma unroll
+      for (int w = 0; w < kGateWarps; ++w) {
+        before += w < warp ? scan[w] : 0;
+        all += scan[w];
+      }
+      if (mk) ent[before + __popc(b & ((1u << lane) - 1))] = make_int2(j, static_cast<int>(mk));
+      if (j == last) stot = mk != 0;
+      total += all;
+      __syncthreads();
+    }
+    if (last >= 0) has_last = stot;
+    if (tid == 0) {
+      const int tail = L - max(last, 0) * A.B;
+      A.seg_tiles[seg] = bad ? -1
+                             : (total - has_last) * A.tiles_per_block +
+                                   (has_last ? (tail + KT - 1) / KT : 0);
+    }
+  }
+  cluster.sync();  // peers' flags stay until rank 0 has read them
+}
+
+// -------------------------------------------------------------------------------------- host
+PagedArgs args_of(const PagedLaunch& L) {
+  PagedArgs A{};
+  const PagedCache& P = L.cache;
+  A.q = static_cast<const __nv_bfloat16*>(L.q);
+  A.k = static_cast<const uint8_t*>(P.k);
+  A.v = static_cast<const uint8_t*>(P.v);
+  A.ks = P.k_scale; A.vs = P.v_scale; A.sums = P.sums;
+  A.page_table = P.page_table; A.seq_lens = P.seq_lens;
+  A.nseq = P.nseq; A.max_pages = P.max_pages; A.num_pages = P.num_pages;
+  A.page_log = P.page_log; A.G = P.G; A.B = P.B;
+  A.rows = L.rows; A.Hq = L.Hq; A.group = L.Hq / P.G;
+  A.nrt = L.shape.nrt; A.nseg = L.shape.nseg;
+  A.topk = L.topk; A.nb_cap = L.shape.nb_cap; A.ent_cap = L.shape.ent_cap;
+  const int kt = kTileBytes / (P.d * (P.fp8 ? 1 : 2));
+  A.tiles_per_block = L.topk ? (P.B + kt - 1) / kt : 0;
+  A.scale_log2 = L.scale * 1.4426950408889634f;
+  A.seg_first = L.seg_first; A.seg_count = L.seg_count;
+  A.part_o = L.part_o; A.part_ml = reinterpret_cast<float2*>(L.part_ml);
+  A.seg_tiles = L.seg_tiles; A.entries = reinterpret_cast<int2*>(L.entries);
+  A.keys = L.keys; A.marks = L.marks;
+  A.idx = L.idx;
+  A.o = static_cast<__nv_bfloat16*>(L.o);
+  A.lse = L.lse;
+  return A;
+}
+
+// Launch attributes are set once per device and kernel (a driver call that a decode step of a few
+// microseconds would notice).
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes, int (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev] >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = bytes;
+  return e;
+}
+
+template <int D, bool FP8, int NT, bool SPARSE>
+cudaError_t attn(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
+  static int done[64];
+  constexpr int smem = kPagedWarps * Tile<D, FP8>::kWarpBytes;
+  cudaError_t e = allow_smem(paged_attn_kernel<D, FP8, NT, SPARSE>, smem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(L.shape.ctas));
+  cfg.blockDim = dim3(kPagedThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = SPARSE ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, FP8, NT, SPARSE>, A);
+}
+
+template <int D, int RR>
+cudaError_t gate(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
+  static int done[64];
+  size_t smem = RR * D * 8 + kGateWarps * RR * 32 * 8 + 32 * (D + 4) * 4 + kGateWarps * 256 * 4;
+  const int in_smem = L.shape.gate_ctas == 1 && !L.shape.gate_global;
+  if (in_smem) smem += static_cast<size_t>(A.nb_cap) * (RR * 8 + 4);
+  cudaError_t e = allow_smem(paged_gate_kernel<D, RR>, static_cast<int>(smem), done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(A.nseg) * L.shape.gate_ctas);
+  cfg.blockDim = dim3(kGateThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(L.shape.gate_ctas);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const int kt = kTileBytes / (D * (L.cache.fp8 ? 1 : 2));
+  return cudaLaunchKernelEx(&cfg, paged_gate_kernel<D, RR>, A, L.shape.rows_per_tile, kt, in_smem);
+}
+
+template <int D>
+cudaError_t merge(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(A.nseq) * A.rows * A.Hq);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, A, L.shape.rows_per_tile, L.topk > 0);
+}
+
+}  // namespace
+
+PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms) {
+  PagedShape S{};
+  const int R = rows * (Hq / P.G);
+  S.rows_per_tile = R <= 8 ? 8 : 16;
+  S.nrt = (R + S.rows_per_tile - 1) / S.rows_per_tile;
+  S.nseg = static_cast<long long>(P.nseq) * P.G * S.nrt;
+  const int kt = kTileBytes / (P.d * (P.fp8 ? 1 : 2));
+  const long long cap = static_cast<long long>(P.max_pages) << P.page_log;
+  const long long tiles = S.nseg * ((cap + kt - 1) / kt);
+  S.ctas = static_cast<int>(std::min<long long>(sms, (tiles + kPagedWarps - 1) / kPagedWarps));
+  S.slots = static_cast<long long>(S.ctas) * kPagedWarps + S.nseg;
+  if (topk) {
+    S.nb_cap = static_cast<int>((cap + P.B - 1) / P.B);
+    S.ent_cap = static_cast<int>(std::min<long long>(
+        S.nb_cap, static_cast<long long>(std::min(R, S.rows_per_tile)) * topk));
+    S.gate_ctas = 1;
+    while (S.gate_ctas < 8 && S.nb_cap > 128 * S.gate_ctas) S.gate_ctas *= 2;
+    const int rr = std::min(R, S.rows_per_tile);
+    // keys and marks of a small cache stay in shared memory
+    S.gate_global = S.gate_ctas > 1 || static_cast<long long>(S.nb_cap) * (rr * 16 + 4) > 65536;
+  }
+  return S;
+}
+
+cudaError_t launch_paged_gate(const PagedLaunch& L, cudaStream_t s) {
+  const PagedArgs A = args_of(L);
+  const int R = std::min(L.rows * A.group, L.shape.rows_per_tile);
+#define MOBA_GATE(D)                                     \
+  return R <= 1   ? gate<D, 1>(A, L, s)                  \
+         : R <= 2 ? gate<D, 2>(A, L, s)                  \
+         : R <= 4 ? gate<D, 4>(A, L, s)                  \
+         : R <= 8 ? gate<D, 8>(A, L, s) : gate<D, 16>(A, L, s)
+  if (L.cache.d == 64) MOBA_GATE(64);
+  MOBA_GATE(128);
+#undef MOBA_GATE
+}
+
+cudaError_t launch_paged_attn(const PagedLaunch& L, cudaStream_t s) {
+  const PagedArgs A = args_of(L);
+  const bool two = L.shape.rows_per_tile == 16, sparse = L.topk > 0;
+#define MOBA_ATTN(D, F)                                                              \
+  return two ? (sparse ? attn<D, F, 2, true>(A, L, s) : attn<D, F, 2, false>(A, L, s)) \
+             : (sparse ? attn<D, F, 1, true>(A, L, s) : attn<D, F, 1, false>(A, L, s))
+  if (L.cache.d == 64) {
+    if (L.cache.fp8) MOBA_ATTN(64, true);
+    MOBA_ATTN(64, false);
+  }
+  if (L.cache.fp8) MOBA_ATTN(128, true);
+  MOBA_ATTN(128, false);
+#undef MOBA_ATTN
+}
+
+cudaError_t launch_paged_merge(const PagedLaunch& L, cudaStream_t s) {
+  const PagedArgs A = args_of(L);
+  return L.cache.d == 64 ? merge<64>(A, L, s) : merge<128>(A, L, s);
+}
+
+}  // namespace moba

@@ -29,7 +29,9 @@ EXPORTS = ["moba_status_string", "moba_version", "moba_workspace_bytes", "moba_c
            "moba_attn_fwd_noalloc", "moba_noalloc_status", "moba_set_wait_limit_ns",
            "moba_centroids_kconv", "moba_attn_fwd_kconv", "moba_decode_workspace_bytes",
            "moba_decode_fwd", "moba_bwd_workspace_bytes", "moba_attn_bwd",
-           "moba_set_diag_stall"]
+           "moba_set_diag_stall", "moba_qk_norm_rope", "moba_qk_norm_rope_bwd_workspace_bytes",
+           "moba_qk_norm_rope_bwd", "moba_cache_append", "moba_cache_read",
+           "moba_paged_workspace_bytes", "moba_paged_attn_fwd", "moba_paged_decode_fwd"]
 
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -94,6 +96,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moba_set_wait_limit_ns.restype = ctypes.c_ulonglong
     lib.moba_set_diag_stall.argtypes = [I]
     lib.moba_set_diag_stall.restype = I
+    lib.moba_qk_norm_rope.argtypes = [P, L, P, L, P, P, P, I, I, P, I, I, I, I, F, I, P, P, P]
+    lib.moba_qk_norm_rope.restype = I
+    lib.moba_qk_norm_rope_bwd_workspace_bytes.argtypes = [I, I, I]
+    lib.moba_qk_norm_rope_bwd_workspace_bytes.restype = S
+    lib.moba_qk_norm_rope_bwd.argtypes = [P, L, P, L, P, P, P, I, I, P, P, P, I, I, I, I, F, I, P,
+                                          P, P, P, P, S, P]
+    lib.moba_qk_norm_rope_bwd.restype = I
+    lib.moba_cache_append.argtypes = [P, P, L, P, L, P, I, P]
+    lib.moba_cache_append.restype = I
+    lib.moba_cache_read.argtypes = [P, P, I, P, P, P]
+    lib.moba_cache_read.restype = I
+    lib.moba_paged_workspace_bytes.argtypes = [P, I, I, I]
+    lib.moba_paged_workspace_bytes.restype = S
+    lib.moba_paged_attn_fwd.argtypes = [P, P, I, I, F, P, P, P, S, P]
+    lib.moba_paged_attn_fwd.restype = I
+    lib.moba_paged_decode_fwd.argtypes = [P, P, I, I, I, F, P, P, P, P, S, P]
+    lib.moba_paged_decode_fwd.restype = I
     _lib = lib
     return lib
 
@@ -469,6 +488,300 @@ def moba_attn_fwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                                               ctypes.c_float(scale), _ptr(o), _ptr(lse),
                                               _stream(stream))
     _check(st, "moba_attn_fwd_noalloc")
+    return o, lse
+
+
+def _rows(what: str, name: str, t: torch.Tensor, heads: Optional[int] = None,
+          d: Optional[int] = None) -> int:
+    """Checks bf16 [T, heads, d] whose heads are packed and whose tokens may lie further apart
+    (a slice of a fused projection); returns the token stride in elements."""
+    if not torch.is_tensor(t) or t.dim() != 3:
+        _bad(what, f"{name} must be a 3-D tensor")
+    if t.dtype != torch.bfloat16:
+        _bad(what, f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    T, h, w = t.shape
+    if (heads is not None and h != heads) or (d is not None and w != d):
+        _bad(what, f"{name} must have shape {(T, heads, d)}, got {tuple(t.shape)}")
+    if (w > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != w):
+        _bad(what, f"{name}: the heads of a token must be packed, strides are {t.stride()}")
+    return t.stride(0) if T > 1 else h * w
+
+
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call. Memory of the caching allocator belongs to the current stream: a
+    call on another stream keeps it from being handed out before that stream is past the call."""
+    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if stream is not None and stream != torch.cuda.current_stream():
+        ws.record_stream(stream)
+    return ws
+
+
+def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """fp32 [n_pos, rot_dim] table for moba_qk_norm_rope: the cosines, then the sines, of
+    p * base^(-2 i / rot_dim), computed in 64 bits (a far position's angle has no bits to spare)."""
+    inv = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+                          / rot_dim)
+    a = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def _check_norm(what, q, k, q_weight, k_weight, rope, positions):
+    q_ld = _rows(what, "q", q)
+    T, hq, d = q.shape
+    dev = _current_device(what, q)
+    k_ld = _rows(what, "k", k, d=d)
+    if k.shape[0] != T or k.device != dev:
+        _bad(what, f"k must have {T} tokens on {dev}, got {tuple(k.shape)} on {k.device}")
+    _want(what, "q_weight", q_weight, torch.float32, (d,), dev)
+    _want(what, "k_weight", k_weight, torch.float32, (d,), dev)
+    if not torch.is_tensor(rope) or rope.dim() != 2:
+        _bad(what, "rope must be a [n_pos, rot_dim] tensor")
+    _want(what, "rope", rope, torch.float32, None, dev)
+    _want(what, "positions", positions, torch.int32, (T,), dev)
+    return dev, T, hq, k.shape[1], d, q_ld, k_ld
+
+
+def moba_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
+                      k_weight: torch.Tensor, rope: torch.Tensor, positions: torch.Tensor,
+                      eps: float = 1e-6, interleaved: bool = False,
+                      q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of every head of q [T, Hq, d] and k [T, Hkv, d] (tokens may be strided) times fp32
+    weights [d], and the rotary position of positions [T] in a table from rope_table. Returns
+    packed (q_out, k_out)."""
+    what = "moba_qk_norm_rope"
+    dev, T, hq, hkv, d, q_ld, k_ld = _check_norm(what, q, k, q_weight, k_weight, rope, positions)
+    if q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _want(what, "q_out", q_out, torch.bfloat16, (T, hq, d), dev)
+    if k_out is None:
+        k_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _want(what, "k_out", k_out, torch.bfloat16, (T, hkv, d), dev)
+    st = load_library().moba_qk_norm_rope(
+        q.data_ptr(), q_ld, k.data_ptr(), k_ld, q_weight.data_ptr(), k_weight.data_ptr(),
+        rope.data_ptr(), rope.shape[0], rope.shape[1], positions.data_ptr(), T, hq, hkv, d, eps,
+        1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), _stream(stream))
+    _check(st, what)
+    return q_out, k_out
+
+
+def moba_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
+                          k_weight: torch.Tensor, rope: torch.Tensor, positions: torch.Tensor,
+                          d_q_out: torch.Tensor, d_k_out: torch.Tensor, eps: float = 1e-6,
+                          interleaved: bool = False, dq: Optional[torch.Tensor] = None,
+                          dk: Optional[torch.Tensor] = None,
+                          d_q_weight: Optional[torch.Tensor] = None,
+                          d_k_weight: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dq, dk, d_q_weight, d_k_weight) of moba_qk_norm_rope; nothing but its inputs is
+    needed from the forward pass."""
+    what = "moba_qk_norm_rope_bwd"
+    dev, T, hq, hkv, d, q_ld, k_ld = _check_norm(what, q, k, q_weight, k_weight, rope, positions)
+    _want(what, "d_q_out", d_q_out, torch.bfloat16, (T, hq, d), dev)
+    _want(what, "d_k_out", d_k_out, torch.bfloat16, (T, hkv, d), dev)
+    dq = torch.empty_like(d_q_out) if dq is None else dq
+    dk = torch.empty_like(d_k_out) if dk is None else dk
+    d_q_weight = torch.empty_like(q_weight) if d_q_weight is None else d_q_weight
+    d_k_weight = torch.empty_like(k_weight) if d_k_weight is None else d_k_weight
+    _want(what, "dq", dq, torch.bfloat16, (T, hq, d), dev)
+    _want(what, "dk", dk, torch.bfloat16, (T, hkv, d), dev)
+    _want(what, "d_q_weight", d_q_weight, torch.float32, (d,), dev)
+    _want(what, "d_k_weight", d_k_weight, torch.float32, (d,), dev)
+    lib = load_library()
+    if workspace is None:
+        workspace = _workspace(int(lib.moba_qk_norm_rope_bwd_workspace_bytes(hq, hkv, d)), dev,
+                               stream)
+    _want(what, "workspace", workspace, torch.uint8, None, dev)
+    st = lib.moba_qk_norm_rope_bwd(
+        q.data_ptr(), q_ld, k.data_ptr(), k_ld, q_weight.data_ptr(), k_weight.data_ptr(),
+        rope.data_ptr(), rope.shape[0], rope.shape[1], positions.data_ptr(), d_q_out.data_ptr(),
+        d_k_out.data_ptr(), T, hq, hkv, d, eps, 1 if interleaved else 0, dq.data_ptr(),
+        dk.data_ptr(), d_q_weight.data_ptr(), d_k_weight.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream(stream))
+    _check(st, what)
+    return dq, dk, d_q_weight, d_k_weight
+
+
+class _CacheStruct(ctypes.Structure):
+    """moba_paged_cache of include/moba.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "block_sums",
+                                               "page_table", "seq_lens")] + \
+               [(n, ctypes.c_int32) for n in ("dtype", "nseq", "max_pages", "num_pages",
+                                              "page_size", "Hkv", "d", "block_size")]
+
+
+class PagedCache:
+    """A paged key-value cache: the caller's tensors, checked once, as the cache calls take them.
+
+    k, v: [num_pages, Hkv, page_size, d], bfloat16 or float8_e4m3fn; k_scale, v_scale (e4m3 only):
+    uint8 [num_pages, Hkv, page_size]; page_table: int32 [nseq, max_pages]; seq_lens: int32 [nseq];
+    block_sums (for moba_paged_decode_fwd): float32 [num_pages, Hkv, d] with its block_size. The
+    tensors are kept by reference and their contents may change between calls; see
+    include/moba.h for the layout and its limits.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
+                 seq_lens: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None,
+                 block_sums: Optional[torch.Tensor] = None, block_size: Optional[int] = None):
+        what = "PagedCache"
+        if not torch.is_tensor(k) or k.dim() != 4:
+            _bad(what, "k must be a [num_pages, Hkv, page_size, d] tensor")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            _bad(what, f"k must be torch.bfloat16 or torch.float8_e4m3fn, got {k.dtype}")
+        _want(what, "k", k, k.dtype, None, _ANY_DEVICE)
+        dev = _current_device(what, k)
+        pages, hkv, page, d = k.shape
+        _want(what, "v", v, k.dtype, (pages, hkv, page, d), dev)
+        if not torch.is_tensor(page_table) or page_table.dim() != 2:
+            _bad(what, "page_table must be a [nseq, max_pages] tensor")
+        _want(what, "page_table", page_table, torch.int32, None, dev)
+        nseq = page_table.shape[0]
+        _want(what, "seq_lens", seq_lens, torch.int32, (nseq,), dev)
+        fp8 = k.dtype == torch.float8_e4m3fn
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if fp8:
+                _want(what, name, t, torch.uint8, (pages, hkv, page), dev)
+            elif t is not None:
+                _bad(what, f"{name} goes with an e4m3 cache")
+        if block_sums is not None:
+            _want(what, "block_sums", block_sums, torch.float32, (pages, hkv, d), dev)
+            if not isinstance(block_size, int) or block_size < 1:
+                _bad(what, "block_sums need a block_size")
+        self.tensors = (k, v, k_scale, v_scale, block_sums, page_table, seq_lens)
+        self.device, self.nseq, self.hkv, self.d = dev, nseq, hkv, d
+        self.block_size = block_size if block_sums is not None else 0
+        ptr = [None if t is None else t.data_ptr() for t in self.tensors]
+        self._c = _CacheStruct(*ptr, 1 if fp8 else 0, nseq, page_table.shape[1], pages, page, hkv,
+                               d, self.block_size)
+        self._ref = ctypes.addressof(self._c)
+        self._bytes = {}
+
+    def workspace_bytes(self, hq: int, rows_per_seq: int = 1, topk: int = 0) -> int:
+        """Bytes of workspace for attention over this cache (topk 0: moba_paged_attn_fwd)."""
+        key = (hq, rows_per_seq, topk)
+        if key not in self._bytes:
+            self._bytes[key] = int(load_library().moba_paged_workspace_bytes(
+                self._ref, hq, rows_per_seq, topk))
+        return self._bytes[key]
+
+    def _here(self, what: str) -> torch.device:
+        """The cache's device, which has to be the current one."""
+        if torch.cuda.current_device() != self.device.index:
+            _bad(what, f"the cache is on {self.device} but the current device is "
+                       f"cuda:{torch.cuda.current_device()}")
+        return self.device
+
+
+def _cache(what: str, cache) -> PagedCache:
+    if not isinstance(cache, PagedCache):
+        _bad(what, "cache must be a PagedCache")
+    return cache
+
+
+def moba_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor,
+                      cu_seqlens_q: torch.Tensor, stream=None) -> None:
+    """Writes the newest rows k, v [Tq, Hkv, d] bf16 (tokens may be strided) of every sequence
+    (cu_seqlens_q [nseq + 1]; cache.seq_lens already counts them) into the cache's pages, rounded
+    to 8 bits where the cache is e4m3, and adds the keys to their blocks' sums."""
+    what = "moba_cache_append"
+    dev = _cache(what, cache)._here(what)
+    k_ld = _rows(what, "k", k, cache.hkv, cache.d)
+    v_ld = _rows(what, "v", v, cache.hkv, cache.d)
+    if v.shape[0] != k.shape[0]:
+        _bad(what, f"k and v must have the same rows, got {k.shape[0]} and {v.shape[0]}")
+    if k.device != dev or v.device != dev:
+        _bad(what, f"k is on {k.device} and v on {v.device}, the cache on {dev}")
+    _want(what, "cu_seqlens_q", cu_seqlens_q, torch.int32, (cache.nseq + 1,), dev)
+    _check(load_library().moba_cache_append(cache._ref, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+                                            cu_seqlens_q.data_ptr(), k.shape[0],
+                                            _stream(stream)), what)
+
+
+def moba_cache_read(cache: PagedCache, cu_seqlens: torch.Tensor, cu_seqlens_host,
+                    k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The first cu[s+1] - cu[s] cached tokens of every sequence, packed: (k, v) [T, Hkv, d] bf16
+    as moba_attn_fwd takes them."""
+    what = "moba_cache_read"
+    dev = _cache(what, cache)._here(what)
+    _want(what, "cu_seqlens", cu_seqlens, torch.int32, (cache.nseq + 1,), dev)
+    if len(cu_seqlens_host) != cache.nseq + 1:
+        _bad(what, f"cu_seqlens_host must have {cache.nseq + 1} entries")
+    shape = (int(cu_seqlens_host[-1]), cache.hkv, cache.d)
+    if shape[0] < 0:
+        _bad(what, "cu_seqlens_host must not be negative")
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    _want(what, "k", k, torch.bfloat16, shape, dev)
+    _want(what, "v", v, torch.bfloat16, shape, dev)
+    _check(load_library().moba_cache_read(cache._ref, cu_seqlens.data_ptr(), shape[0],
+                                          k.data_ptr(), v.data_ptr(), _stream(stream)), what)
+    return k, v
+
+
+def _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace, stream):
+    """Checks and buffers that both attention calls over a paged cache share."""
+    dev = _cache(what, cache)._here(what)
+    if not torch.is_tensor(q) or q.dim() != 3:
+        _bad(what, "q must be a 3-D tensor")
+    n, hq, d = q.shape
+    if rows_per_seq < 1 or n != cache.nseq * rows_per_seq or d != cache.d:
+        _bad(what, f"q must have shape {(cache.nseq * rows_per_seq, hq, cache.d)}, "
+                   f"got {tuple(q.shape)}")
+    _want(what, "q", q, torch.bfloat16, None, dev)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _want(what, "o", o, torch.bfloat16, (n, hq, d), dev)
+    if lse is None:
+        lse = torch.empty((hq, n), dtype=torch.float32, device=dev)
+    else:
+        _want(what, "lse", lse, torch.float32, (hq, n), dev)
+    if workspace is None:
+        workspace = _workspace(cache.workspace_bytes(hq, rows_per_seq, topk), dev, stream)
+    else:
+        _want(what, "workspace", workspace, torch.uint8, None, dev)
+    return dev, n, hq, o, lse, workspace
+
+
+def moba_paged_attn_fwd(cache: PagedCache, q: torch.Tensor, rows_per_seq: int = 1,
+                        scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                        lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Full attention of the last rows_per_seq tokens of every cached sequence: q
+    [nseq * rows_per_seq, Hq, d] bf16; returns (o like q, lse [Hq, rows] fp32)."""
+    what = "moba_paged_attn_fwd"
+    dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, 0, o, lse, workspace, stream)
+    st = load_library().moba_paged_attn_fwd(
+        cache._ref, q.data_ptr(), hq, rows_per_seq, cache.d ** -0.5 if scale is None else scale,
+        o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, what)
+    return o, lse
+
+
+def moba_paged_decode_fwd(cache: PagedCache, q: torch.Tensor, topk: int, rows_per_seq: int = 1,
+                          scale: Optional[float] = None,
+                          block_idx_out: Optional[torch.Tensor] = None,
+                          o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """MoBA attention of the last rows_per_seq tokens of every cached sequence: routing by the
+    cache's block_sums, then attention over the selected blocks. Returns (o, lse) as
+    moba_paged_attn_fwd; block_idx_out [Hq, rows, topk] int32 receives the routing."""
+    what = "moba_paged_decode_fwd"
+    if topk < 1 or not _cache(what, cache).block_size:
+        _bad(what, "topk must be positive and the cache have block_sums")
+    dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace, stream)
+    if block_idx_out is not None:
+        _want(what, "block_idx_out", block_idx_out, torch.int32, (hq, n, topk), dev)
+    st = load_library().moba_paged_decode_fwd(
+        cache._ref, q.data_ptr(), hq, rows_per_seq, topk,
+        cache.d ** -0.5 if scale is None else scale,
+        None if block_idx_out is None else block_idx_out.data_ptr(), o.data_ptr(), lse.data_ptr(),
+        ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, what)
     return o, lse
 
 

@@ -185,6 +185,136 @@ int moba_decode_fwd(const void* q, const void* k_cache, const void* v_cache,
                     size_t workspace_bytes, void* stream);
 
 /*
+ * RMS norm of every query and key head with the rotary position embedding in the same pass (what
+ * stands between a layer's projection and moba_attn_fwd, or a cache's next row). For each token t
+ * and head, x the d elements of that head and p = positions[t]:
+ *   z = x * (mean(x^2) + eps)^-1/2 * weight,
+ *   y = z with the pairs of its first rot_dim elements turned: (a, b) -> (a c - b s, b c + a s),
+ *   c = rope[p, i], s = rope[p, rot_dim / 2 + i] for pair i.
+ * interleaved = 0: pair i is (z[i], z[i + rot_dim / 2]); 1: (z[2 i], z[2 i + 1]).
+ * q, k         : bf16; token t's heads are packed [Hq, d] (k: [Hkv, d]) at q + t * q_stride
+ *                elements, so both may be slices of one fused projection's rows. Strides are
+ *                multiples of 8, at least Hq * d and Hkv * d.
+ * q_weight, k_weight: fp32 [d]. rope: fp32 [n_pos, rot_dim], cosines then sines (the caller's
+ *                table, so any base or scaling of the angles). positions: int32 [T]; a token whose
+ *                position lies outside the table becomes NaN.
+ * rot_dim      : a multiple of 16, 16 .. d; the elements behind it are normed and not turned.
+ * q_out, k_out : bf16 [T, Hq, d], [T, Hkv, d]. May be q and k themselves when those are packed;
+ *                no other overlap.
+ * fp32 arithmetic, rounded once. HBM-bound: every element is read once and written once.
+ */
+int moba_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride,
+                      const float* q_weight, const float* k_weight, const float* rope, int n_pos,
+                      int rot_dim, const int32_t* positions, int T, int Hq, int Hkv, int d,
+                      float eps, int interleaved, void* q_out, void* k_out, void* stream);
+
+/*
+ * Gradients of moba_qk_norm_rope. d_q_out, d_k_out: bf16 [T, Hq, d], [T, Hkv, d], the gradients of
+ * its outputs; the other inputs as given to it (nothing else is kept from the forward pass).
+ * With r = (mean(x^2) + eps)^-1/2 and dz = d_out turned back:
+ *   d_weight = sum over tokens and heads of dz * x r,
+ *   dx = r (dz weight - x r mean(dz weight x r)).
+ * dq, dk: bf16 [T, Hq, d], [T, Hkv, d], no overlap with q, k (dq may be d_q_out, dk d_k_out);
+ * d_q_weight, d_k_weight: fp32 [d] (written, zero when T = 0; the same bits every time).
+ * workspace: at least moba_qk_norm_rope_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+size_t moba_qk_norm_rope_bwd_workspace_bytes(int Hq, int Hkv, int d);
+int moba_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long long k_stride,
+                          const float* q_weight, const float* k_weight, const float* rope,
+                          int n_pos, int rot_dim, const int32_t* positions, const void* d_q_out,
+                          const void* d_k_out, int T, int Hq, int Hkv, int d, float eps,
+                          int interleaved, void* dq, void* dk, float* d_q_weight,
+                          float* d_k_weight, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * A paged key-value cache of nseq sequences, all buffers the caller's.
+ *   k, v       [num_pages, Hkv, page_size, d]: bf16, or e4m3 codes. Token u of sequence s is in
+ *              page page_table[s, u / page_size], slot u % page_size.
+ *   k_scale, v_scale  e4m3: uint8 [num_pages, Hkv, page_size], a row's power of two as a biased
+ *              exponent: value = code * 2^(byte - 127). NULL for bf16.
+ *   block_sums nullable fp32 [num_pages, Hkv, d]: the sum of the keys of each MoBA block (before
+ *              any rounding to 8 bits), kept at the block's first page; moba_paged_decode_fwd
+ *              scores blocks by it.
+ *   page_table int32 [nseq, max_pages], seq_lens int32 [nseq] (the newest rows included), both on
+ *              the device: they may change between calls, and between replays of a graph.
+ *   page_size  a power of two, 16 .. 4096; block_size (read with block_sums only): a multiple of
+ *              64 and of page_size. max_pages * page_size <= 2^30, Hkv <= 1024.
+ * Entries of page_table behind a sequence's last page are not read. A page number outside
+ * [0, num_pages), or a seq_lens beyond max_pages * page_size, is never dereferenced: the calls
+ * below say what becomes of it. Two sequences may share pages that no call writes.
+ */
+#define MOBA_CACHE_BF16 0
+#define MOBA_CACHE_E4M3 1
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  float* block_sums;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  int32_t dtype, nseq, max_pages, num_pages, page_size, Hkv, d, block_size;
+} moba_paged_cache;
+
+/*
+ * Writes new rows into the cache: cu_seqlens_q_dev int32 [nseq + 1] (cuq[0] = 0, non-decreasing,
+ * cuq[nseq] = Tq) gives n_s = cuq[s+1] - cuq[s] rows of sequence s, its last n_s tokens (positions
+ * seq_lens[s] - n_s ...; seq_lens already counts them). k, v: bf16, token strides in elements as
+ * in moba_qk_norm_rope (at least Hkv * d, multiples of 8).
+ *   e4m3: a row of d keys (values) is stored as RN_e4m3(x / 2^e), 2^e the smallest power of two
+ *   >= 2^-126 that keeps its largest magnitude within 448.
+ *   block_sums (when given): blocks that begin with a new row are set to the sum of their new
+ *   keys, a block that was begun before is added to. Column sums in a fixed order, fp32.
+ * Rows whose page is outside the pool, whose position is negative or at or behind
+ * max_pages * page_size, and rows at or behind cuq[nseq] are not written. No page may receive
+ * rows of two sequences in one call.
+ */
+int moba_cache_append(const moba_paged_cache* cache, const void* k, long long k_stride,
+                      const void* v, long long v_stride, const int32_t* cu_seqlens_q_dev, int Tq,
+                      void* stream);
+
+/*
+ * Reads cached rows back, packed: the first cu[s+1] - cu[s] tokens of every sequence into
+ * k, v bf16 [T, Hkv, d] (T = cu[nseq]; e4m3 values widen exactly), as moba_attn_fwd takes them.
+ * Rows at or behind seq_lens[s] are zeros, rows in a page outside the pool NaN.
+ */
+int moba_cache_read(const moba_paged_cache* cache, const int32_t* cu_seqlens_dev, int T, void* k,
+                    void* v, void* stream);
+
+/*
+ * Attention of the newest rows over a paged cache: the last rows_per_seq tokens of every sequence
+ * (1 for a decode step), q bf16 [nseq * rows_per_seq, Hq, d], row s * rows_per_seq + r at position
+ * seq_lens[s] - rows_per_seq + r. Each row attends the keys up to its own position:
+ *   moba_paged_attn_fwd    all of them (a layer with full attention);
+ *   moba_paged_decode_fwd  those of the blocks that the MoBA gate selects, as moba_decode_fwd:
+ *     its current block and the topk - 1 past blocks with the largest q . block_sums (past blocks
+ *     are full, so the order is that of the centroids; scored in fp64; equal scores: the lower
+ *     block). block_idx_out: nullable int32 [Hq, nseq * rows_per_seq, topk], ascending, -1 padded.
+ * o: bf16 [nseq * rows_per_seq, Hq, d]; lse: fp32 [Hq, nseq * rows_per_seq]. A row without a
+ * position (seq_lens[s] < rows_per_seq) gives o = 0, lse = -inf and -1s. A sequence that needs a
+ * page outside the pool, or more pages than max_pages, gives NaN in its rows of o and lse; the
+ * other sequences' rows are right. The same call on the same contents gives the same bits; how a
+ * sequence is cut over the SMs depends on all lengths of the call, so the last bits of its rows may
+ * differ in another batch. Cached values that a row must not see may be anything in rows at
+ * or behind seq_lens[s]; values of cached rows are to be finite.
+ * workspace: at least moba_paged_workspace_bytes(...) (topk 0 for moba_paged_attn_fwd; depends on
+ * the sizes alone, not on lengths), 256-byte aligned, for one call at a time; it holds nothing
+ * between calls.
+ * Limits: rows_per_seq <= 256, Hq / Hkv <= 256, topk <= 64, at most 32768 blocks per sequence
+ * (max_pages * page_size / block_size). HBM-bound: each cached row that a group of up to 16 rows
+ * of a kv head attends is read once.
+ */
+size_t moba_paged_workspace_bytes(const moba_paged_cache* cache, int Hq, int rows_per_seq,
+                                  int topk);
+int moba_paged_attn_fwd(const moba_paged_cache* cache, const void* q, int Hq, int rows_per_seq,
+                        float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                        void* stream);
+int moba_paged_decode_fwd(const moba_paged_cache* cache, const void* q, int Hq, int rows_per_seq,
+                          int topk, float scale, int32_t* block_idx_out, void* o, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Backward pass of the routed attention [MoBA README, "Introducing MoBA": trainable block sparse
  * attention]. The routing is held fixed: the top-k gate is piecewise constant in q and the
  * centroids, so no gradient flows through the selection (as in top-k mixture-of-experts routing).
@@ -281,9 +411,11 @@ int moba_set_diag_stall(int on);
  * recorded events and writes, for each kernel class, the summed device milliseconds and launch
  * count since the last reset; kernel classes, in order: centroid, gate, route_count, route_scan,
  * route_scatter, attention, merge, plan, densify (d = 64: the routed query rows copied into one
- * dense array), decode (moba_decode_fwd's kernels), bwd_dkdv, bwd_dq and bwd_aux (moba_attn_bwd's
- * key-stationary and query-stationary kernels, and its D / dQ conversion passes). Returns the
- * number of classes (13), or a negative status.
+ * dense array), decode (the kernels of moba_decode_fwd and of the attention over a paged cache),
+ * bwd_dkdv, bwd_dq and bwd_aux (moba_attn_bwd's
+ * key-stationary and query-stationary kernels, and its D / dQ conversion passes). The norm and
+ * cache kernels have NVTX ranges and are counted, and belong to no timed class. Returns the number
+ * of classes (13), or a negative status.
  */
 int moba_timing_enable(int enable);
 int moba_timing_reset(void);
