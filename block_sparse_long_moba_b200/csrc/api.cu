@@ -780,7 +780,7 @@ int check_norm(const void* q, long long q_ld, const void* k, long long k_ld, con
   if (d != 64 && d != 128) return MOBA_ERR_UNSUPPORTED;
   if (Hq > 65536 || Hkv > 65536) return MOBA_ERR_UNSUPPORTED;
   // the grid has one warp per token and chunk of up to 16 heads
-  if (static_cast<long long>(T) * (static_cast<long long>(Hq) + Hkv) >= (1LL << 33))
+  if (static_cast<long long>(T) * (static_cast<long long>(Hq) + Hkv) >= (1LL << 31))
     return MOBA_ERR_UNSUPPORTED;
   if (rot < 16 || rot > d || rot % 16 != 0) return MOBA_ERR_UNSUPPORTED;
   if (q_ld < static_cast<long long>(Hq) * d || k_ld < static_cast<long long>(Hkv) * d ||
@@ -902,7 +902,7 @@ int check_cache(const moba_paged_cache* c, PagedCache* P) {
   return MOBA_OK;
 }
 
-struct PagedLayout { size_t seg_first, seg_count, part_o, part_ml, seg_tiles, entries, keys,
+struct PagedLayout { size_t seg_desc, part_o, part_ml, seg_tiles, entries, keys,
                      marks, total; };
 
 PagedLayout paged_layout(const PagedShape& S, int d, int topk) {
@@ -911,8 +911,7 @@ PagedLayout paged_layout(const PagedShape& S, int d, int topk) {
   auto take = [&](size_t bytes) { const size_t at = o; o = up256(o + bytes); return at; };
   const size_t nseg = static_cast<size_t>(S.nseg);
   const size_t rows = static_cast<size_t>(S.slots) * S.rows_per_tile;
-  L.seg_first = take(nseg * 4);
-  L.seg_count = take(nseg * 4);
+  L.seg_desc = take(nseg * 8);
   L.part_o = take(rows * d * 4);
   L.part_ml = take(rows * 8);
   L.seg_tiles = take(topk ? nseg * 4 : 0);
@@ -954,8 +953,7 @@ int paged_run(const moba_paged_cache* c, const void* q, int Hq, int rows, int to
   if (workspace_bytes < L.total) return MOBA_ERR_WORKSPACE;
   if ((st = device_check(nullptr)) != MOBA_OK) return st;
   D.q = q; D.rows = rows; D.Hq = Hq; D.topk = topk; D.scale = scale;
-  D.seg_first = at<int>(workspace, L.seg_first);
-  D.seg_count = at<int>(workspace, L.seg_count);
+  D.seg_desc = at<int>(workspace, L.seg_desc);
   D.part_o = at<float>(workspace, L.part_o);
   D.part_ml = at<float>(workspace, L.part_ml);
   D.seg_tiles = at<int>(workspace, L.seg_tiles);

@@ -78,12 +78,28 @@ struct AppendArgs {
   int Tq, heads;  // heads: kv heads per CTA
 };
 
+// Largest s in [0, n) with key(s) <= x (key non-decreasing, key(0) <= x): 32 probes at a time, so
+// two or three dependent loads where halving would take log2 n. All lanes of the warp call it.
+template <class F>
+__device__ __forceinline__ int last_not_above(int n, int x, F key) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned ok = __ballot_sync(0xffffffffu, at < hi && key(at) <= x);
+    const int p = max(31 - __clz(ok), 0);
+    lo += p * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 // First unit of sequence s: a sequence with n new rows touches at most n / B + 2 blocks, and
 // cuq[s] / B + 2 s leaves room for that without a scan over the sequences before it.
 __device__ __forceinline__ int first_unit(int cuq_s, int s, int B) { return cuq_s / B + 2 * s; }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const AppendArgs A) {
+__global__ void __launch_bounds__(kCacheThreads, 3) cache_append_kernel(const AppendArgs A) {
   constexpr int LPR = D / 8;               // lanes per row
   constexpr int SLOTS = kCacheThreads / LPR;
   constexpr int U = 4;                     // rows in flight per lane group
@@ -93,12 +109,10 @@ __global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const Appen
   const int CS = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
   const int unit = blockIdx.x / CS;
-  int lo = 0, hi = C.nseq;  // largest s with first_unit(s) <= unit
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first_unit(__ldg(A.cuq + mid), mid, C.B) <= unit) lo = mid; else hi = mid;
-  }
-  const int s = lo, c0 = __ldg(A.cuq + s), c1 = __ldg(A.cuq + s + 1);
+  const int s = last_not_above(C.nseq, unit, [&](int x) {
+    return first_unit(__ldg(A.cuq + x), x, C.B);
+  });
+  const int c0 = __ldg(A.cuq + s), c1 = __ldg(A.cuq + s + 1);
   const int L = __ldg(C.seq_lens + s);
   // host and device copies may disagree: rows outside the buffers are never touched
   const int n = (c0 >= 0 && c1 >= c0 && c1 <= A.Tq) ? c1 - c0 : 0;
@@ -211,9 +225,9 @@ struct ReadArgs {
   int T;
 };
 
-// kReadRows consecutive packed rows per CTA; thread t < kReadRows finds row t's sequence, page and
-// slot, then d / 8 lanes copy one head's row.
-constexpr int kReadRows = 32;
+// kReadRows consecutive packed rows per CTA; lane t of its first warp finds row t's sequence, page
+// and slot, then d / 8 lanes copy one head's row.
+constexpr int kReadRows = 32;  // a warp
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const ReadArgs A) {
@@ -222,16 +236,14 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const ReadArg
   const CacheView& C = A.C;
   const int r0 = blockIdx.x * kReadRows;
   const int nr = min(kReadRows, A.T - r0);
-  if (threadIdx.x < nr) {
+  if (threadIdx.x < 32) {  // kReadRows rows, one per lane
+    const int s0 = last_not_above(C.nseq, r0, [&](int x) { return __ldg(A.cu + x); });
     const int r = r0 + threadIdx.x;
-    int lo = 0, hi = C.nseq;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(A.cu + mid) <= r) lo = mid; else hi = mid;
-    }
+    int lo = s0;  // the rows of a CTA mostly lie in one sequence
+    while (lo + 1 < C.nseq && __ldg(A.cu + lo + 1) <= r) ++lo;
     const long long u = static_cast<long long>(r) - __ldg(A.cu + lo);
     long long x = -1;
-    if (u >= 0 && u < __ldg(C.seq_lens + lo) && r < __ldg(A.cu + lo + 1)) {
+    if (r < A.T && u >= 0 && u < __ldg(C.seq_lens + lo) && r < __ldg(A.cu + lo + 1)) {
       x = -2;
       if ((u >> C.page_log) < C.max_pages) {
         const int pid = __ldg(C.page_table + static_cast<size_t>(lo) * C.max_pages +
@@ -322,11 +334,12 @@ cudaError_t append(const PagedCache& P, AppendArgs A, int sms, cudaStream_t s) {
   const long long rows = std::min<long long>(B, std::max<long long>(1, A.Tq / P.nseq));
   int cs = 1;
   while (cs < 8 && rows / (2 * cs) >= 64) cs *= 2;
-  // As many kv heads per CTA as fit its threads (their rows are neighbours in the input), fewer
-  // while the grid would not fill the SMs a few times.
+  // As many kv heads per CTA as fit its threads (their rows are neighbours in the input); where a
+  // CTA has several passes of rows to write, fewer while the grid would not fill the SMs.
   int heads = std::min(P.G, SLOTS);
   const long long busy = std::max<long long>(1, A.Tq / B + P.nseq) * cs;
-  while (heads > 1 && busy * ((P.G + heads - 1) / heads) < 4ll * sms) heads = (heads + 1) / 2;
+  while (heads > 1 && rows / cs > 8 && busy * ((P.G + heads - 1) / heads) < 4ll * sms)
+    heads = (heads + 1) / 2;
   A.heads = heads;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * cs), (P.G + heads - 1) / heads);

@@ -218,7 +218,7 @@ struct PagedLaunch {
   const void* q;  // bf16 [nseq * rows, Hq, d]
   int rows, Hq, topk;  // topk 0: dense
   float scale;
-  int *seg_first, *seg_count, *seg_tiles, *entries;
+  int *seg_desc, *seg_tiles, *entries;
   float *part_o, *part_ml;
   unsigned long long* keys;
   unsigned int* marks;

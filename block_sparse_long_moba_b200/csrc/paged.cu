@@ -2,7 +2,8 @@
 // key (dense), or over the blocks that the MoBA gate selects. Pages and scales as in kv_cache.cu.
 //
 // A segment is (sequence s, kv head g, row tile): up to kRows = 8 NT of the rows_per_seq * (Hq/Hkv)
-// rows that share kv head g. Its keys are cut into tiles of 8 KB of K and 8 KB of V. The tiles of
+// rows that share kv head g. Its keys are cut into tiles of 8 KB (e4m3: 4 KB) of K
+// and as much of V. The tiles of
 // all segments form one line, split evenly over the warps of a grid of one CTA per SM, so one
 // long sequence, many short ones and a ragged batch all load every SM alike (the host need not
 // know the lengths). Each warp is on its own: it streams its tiles through a private ring in
@@ -20,11 +21,13 @@
 //
 // e4m3 caches: codes widen exactly to f16, products run in f16 with fp32 accumulation. q is bf16
 // and becomes f16 exactly after a power-of-two scaling of its row (elements 2^-25 below the row's
-// largest round to zero); a key's scale multiplies its logit in fp32; a value's scale goes into
-// the weight p relative to the largest scale seen, by powers of two. p is kept at 2^15 times its
-// value, so that weights down to 2^-29 of the largest stay normal f16 numbers.
-// Rounding: p to bf16 (e4m3 cache: f16) for the second product; logits, maxima, sums (of the
-// unrounded p) and outputs are fp32 until the final bf16.
+// largest round to zero); a key's scale multiplies its logit z in fp32. A value's scale 2^e goes
+// into the weight: w = 2^(z + e - max(z + e) + 15), so that whatever the scales of a sequence are,
+// the terms that matter most to a sum are the normal f16 numbers up to 2^15 and terms below 2^-29 of
+// them lose digits, while the sum of the weights keeps a maximum of its own (per lane, joined at
+// the segment's end).
+// Rounding: weights to bf16 (e4m3 cache: f16) for the second product; logits, maxima, sums (of the
+// unrounded weights) and outputs are fp32 until the final bf16.
 #include <algorithm>
 #include <cfloat>
 #include <cooperative_groups.h>
@@ -41,16 +44,23 @@ namespace moba {
 
 namespace {
 
-constexpr int kPagedWarps = 4;
-constexpr int kPagedThreads = kPagedWarps * 32;
+// Warps of a CTA and bytes of K (and of V) per stage: 192 KB of ring either way. An e4m3 tile takes
+// about 930 instructions per 64 keys, a third of them widening codes, so one warp per scheduler
+// cannot keep up with HBM on its dependent steps; two with half the tile can (8 x 128K tokens:
+// measured 365 us with 4 warps and 8 KB, see the figures at the kernel).
+__host__ __device__ constexpr int paged_warps(bool fp8) { return fp8 ? 8 : 4; }
+__host__ __device__ constexpr int tile_bytes(bool fp8) { return fp8 ? 4096 : 8192; }
 constexpr int kStages = 3;
-constexpr int kTileBytes = 8192;  // of K, and of V, per stage
+constexpr int kNoLimit = 0x7fffffff;
 
 // ------------------------------------------------------------------------------ PTX wrappers
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 16 : 0;  // 0 bytes read: the destination is filled with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -92,13 +102,26 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two e4m3 codes (low 16 bits) -> two f16, exact
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+// two e4m3 codes (the low or high 16 bits) -> two f16, exact
+__device__ __forceinline__ uint32_t widen_lo(uint32_t codes) {
   uint32_t r;
-  asm("{\n .reg .b16 lo;\n cvt.u16.u32 lo, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}"
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}"
       : "=r"(r)
       : "r"(codes));
   return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t codes) {
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}"
+      : "=r"(r)
+      : "r"(codes));
+  return r;
+}
+// 2^x to 2 ulp; results below 2^-126 are 0
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -128,8 +151,7 @@ struct PagedArgs {
   int topk, nb_cap, ent_cap, tiles_per_block;
   float scale_log2;
   // workspace
-  int* seg_first;        // [nseg] first worker of a split segment
-  int* seg_count;        // [nseg] its workers; 1: written directly
+  int2* seg_desc;        // [nseg] first worker of a segment, its workers (1: written directly)
   float* part_o;         // [slots][kRows][D]
   float2* part_ml;       // [slots][kRows]
   int* seg_tiles;        // sparse: [nseg] tiles, -1: a page outside the pool
@@ -172,11 +194,20 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 
 template <int D, bool FP8>
 struct Tile {
+  static constexpr int kWarps = paged_warps(FP8), kThreads = 32 * kWarps;
+  static constexpr int kTileBytes = tile_bytes(FP8);
   static constexpr int RB = D * (FP8 ? 1 : 2);  // bytes of a row
-  static constexpr int KT = kTileBytes / RB;    // keys: 32, 64 or 128
+  static constexpr int KT = kTileBytes / RB;    // keys: 32 or 64
   static constexpr int kScaleBytes = FP8 ? 2 * KT : 0;
   static constexpr int kStage = 2 * kTileBytes + kScaleBytes;
   static constexpr int kWarpBytes = kStages * kStage;
+};
+
+// Keys of one softmax step. 64 where the registers allow: four independent chains of products
+// instead of two, and half the maxima, shuffles and rescaling checks per key.
+template <int D, bool FP8, int NT>
+struct Sub {
+  static constexpr int value = (NT == 1 && Tile<D, FP8>::KT >= 64) ? 64 : 32;
 };
 
 // ------------------------------------------------------------------------------ attention
@@ -186,10 +217,13 @@ __device__ __forceinline__ long long range_start(long long U, int w, int n) {
 }
 
 template <int D, bool FP8, int NT, bool SPARSE>
-__global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const PagedArgs A) {
+__global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(const PagedArgs A) {
   using TL = Tile<D, FP8>;
+  constexpr int kPagedWarps = TL::kWarps, kPagedThreads = TL::kThreads;
+  constexpr int kTileBytes = TL::kTileBytes;
   constexpr int RB = TL::RB, KT = TL::KT, kRows = 8 * NT, CPR = RB / 16;
   constexpr int KS = D / 16;
+  constexpr int SUB = Sub<D, FP8, NT>::value, MT = SUB / 16;  // keys per softmax step, m-tiles
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ long long prefix[kPagedThreads + 1];
   __shared__ int4 ring[kPagedWarps][4];  // tiles in flight: segment, first key, keys | flags, rows
@@ -320,31 +354,62 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
     ++l_tile;
     --l_left;
   };
+  // This lane's 16-byte pieces of 16 rows: piece i is row i * kRowsPer + lane / CPR, column
+  // lane % CPR. Its swizzled place is that of piece 0 with the row's bits above lane / CPR flipped
+  // in, so a full tile costs one xor and two copies per piece.
+  constexpr int kPieces = 16 * CPR / 32, kRowsPer = 32 / CPR;
+  constexpr int kBits = RB == 64 ? 0 : 7;  // bits of a row that the swizzle sees, above my_row's
+  const int my_row = lane / CPR, my_col = lane % CPR;
+  const uint32_t my_dst = swz<RB>(my_row, my_col), my_src = my_row * RB + my_col * 16;
   auto issue = [&](int stage, int slot4) {  // copies of the pending tile into `stage`
     if (pend.x >= 0) {
       if (lane == 0) ring[warp][slot4] = pend;
       const int nk = pend.z & 0xffff, mask = (1 << A.page_log) - 1;
-      const uint32_t kd = wsm + stage * TL::kStage, vd = kd + kTileBytes;
+      const uint32_t kd = wsm + stage * TL::kStage;
+      if (pend.z == KT) {  // all keys there, all pages good
+        const uint8_t *ks = nullptr, *vs = nullptr;
+        const uint8_t* ss = nullptr;
 #pragma unroll
-      for (int gq = 0; gq < KT / 16; ++gq) {  // 16 keys of one page
-        const int pid = __shfl_sync(0xffffffffu, my_pid, gq);
-        const size_t row0 =
-            ((static_cast<size_t>(max(pid, 0)) * A.G + pend_g) << A.page_log) +
-            ((pend.y + gq * 16) & mask);
-        constexpr int kPerLane = 16 * CPR / 32;  // 16-byte pieces of 16 rows per lane
+        for (int gq = 0; gq < KT / 16; ++gq) {  // 16 keys of one page
+          const int at = (pend.y + gq * 16) & mask;
+          if (gq == 0 || at == 0) {
+            const int pid = __shfl_sync(0xffffffffu, my_pid, gq);
+            const size_t row = ((static_cast<size_t>(pid) * A.G + pend_g) << A.page_log) + at;
+            ks = A.k + row * RB + my_src - gq * 16 * RB;
+            vs = A.v + row * RB + my_src - gq * 16 * RB;
+            if (FP8) ss = (lane ? A.vs : A.ks) + row - gq * 16;
+          }
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-          const int piece = i * 32 + lane, r = piece / CPR, cc = piece % CPR;
-          const bool ok = pid >= 0 && gq * 16 + r < nk;
-          const size_t off = (row0 + r) * RB + cc * 16;
-          const uint32_t d = swz<RB>(gq * 16 + r, cc);
-          cp_async16(kd + d, A.k + (ok ? off : 0), ok);
-          cp_async16(vd + d, A.v + (ok ? off : 0), ok);
+          for (int i = 0; i < kPieces; ++i) {
+            const uint32_t d = kd + gq * 16 * RB + i * kRowsPer * RB +
+                               (my_dst ^ (((i * kRowsPer) & kBits) << 4));
+            cp_async16_all(d, ks + (gq * 16 + i * kRowsPer) * RB);
+            cp_async16_all(d + kTileBytes, vs + (gq * 16 + i * kRowsPer) * RB);
+          }
+          if (FP8 && lane < 2)  // 16 scale bytes of K (lane 0) and V (lane 1)
+            cp_async16_all(kd + 2 * kTileBytes + lane * KT + gq * 16, ss + gq * 16);
         }
-        if (FP8 && lane < 2) {  // 16 scale bytes of K (lane 0) and V (lane 1)
-          const bool ok = pid >= 0 && gq * 16 < nk;
-          cp_async16(vd + kTileBytes + lane * KT + gq * 16,
-                     (lane ? A.vs : A.ks) + (ok ? row0 : 0), ok);
+      } else {
+#pragma unroll 1
+        for (int gq = 0; gq < KT / 16; ++gq) {
+          const int pid = __shfl_sync(0xffffffffu, my_pid, gq);
+          const size_t row =
+              ((static_cast<size_t>(max(pid, 0)) * A.G + pend_g) << A.page_log) +
+              ((pend.y + gq * 16) & mask);
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const bool ok = pid >= 0 && gq * 16 + i * kRowsPer + my_row < nk;
+            const size_t off = ok ? (row + i * kRowsPer) * RB + my_src : 0;
+            const uint32_t d = kd + gq * 16 * RB + i * kRowsPer * RB +
+                               (my_dst ^ (((i * kRowsPer) & kBits) << 4));
+            cp_async16(d, A.k + off, ok);
+            cp_async16(d + kTileBytes, A.v + off, ok);
+          }
+          if (FP8 && lane < 2) {
+            const bool ok = pid >= 0 && gq * 16 < nk;
+            cp_async16(kd + 2 * kTileBytes + lane * KT + gq * 16,
+                       (lane ? A.vs : A.ks) + (ok ? row : 0), ok);
+          }
         }
       }
     }
@@ -364,9 +429,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
   Seg id{0, 0, 0};
   uint32_t qf[KS][NT][2];
   float acc[KS][NT][4];
-  float m[NT][2], l[NT][2], cmul[NT][2];
+  // m: maximum of the logits z, in log2 units (e4m3: of z + the value scale's exponent); l: sum of
+  // 2^(z - m) (e4m3: of 2^(z - r), r this lane's own maximum of z)
+  float m[NT][2], l[NT][2], r[NT][2], cmul[NT][2];
   int lim[NT][2];
-  int vref = 0;
   bool bad = false;
   long long cur_begin = seg_begin;  // first tile of the current segment on the line
   int cur_tiles = 0;
@@ -418,8 +484,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
       for (int j = 0; j < 2; ++j) {
         cmul[nt][j] = FP8 ? __shfl_sync(0xffffffffu, f, (2 * c + j) * 4) : f;
         const int rc = id.rt * kRows + nt * 8 + 2 * c + j;  // row of this lane's result columns
-        lim[nt][j] = rc < R ? L - A.rows + rc / A.group + 1 : 0;  // keys it may see
-        m[nt][j] = -INFINITY;
+        // keys it may see; a column of padding (q = 0, never written) needs no mask
+        lim[nt][j] = rc < R ? L - A.rows + rc / A.group + 1 : kNoLimit;
+        m[nt][j] = r[nt][j] = -INFINITY;
         l[nt][j] = 0.f;
       }
 #pragma unroll
@@ -427,7 +494,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[ds][nt][x] = 0.f;
     }
-    vref = 0;
   };
 
   auto finish = [&](int sg, int t0, int t1) {  // this warp had tiles [t0, t1) of the segment
@@ -441,26 +507,31 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
         while (range_start(U, w0 + 1, workers) <= cur_begin) ++w0;
         while (range_start(U, w0, workers) > cur_begin) --w0;
       }
-      A.seg_first[sg] = w0;
-      A.seg_count[sg] = me - w0 + 1;
+      A.seg_desc[sg] = make_int2(w0, me - w0 + 1);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float s = l[nt][j];
+        const float nan = __int_as_float(0x7fffffff);
+        float s = l[nt][j], top = m[nt][j], mul;
+        if (FP8) {
+          top = r[nt][j];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          s = s > 0.f ? s * ex2(r[nt][j] - top) : 0.f;
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float nan = __int_as_float(0x7fffffff);
-        float mul = s > 0.f ? 1.f / s : 0.f;
-        if (FP8) mul *= __uint_as_float(static_cast<uint32_t>(max(vref, 1)) << 23);
-        float top = FP8 ? m[nt][j] - 15.f : m[nt][j];
+        mul = s > 0.f ? 1.f / s : 0.f;
+        if (FP8 && s > 0.f) mul *= ex2(m[nt][j] - 15.f - top);
         if (bad) mul = top = nan;
         const int col = nt * 8 + 2 * c + j, rr = id.rt * kRows + col;
         if (rr >= R) continue;
         if (whole) {
-          const int r = rr / A.group, h = id.g * A.group + rr % A.group;
-          const size_t row = static_cast<size_t>(id.s) * A.rows + r;
+          const int tok = rr / A.group, h = id.g * A.group + rr % A.group;
+          const size_t row = static_cast<size_t>(id.s) * A.rows + tok;
           __nv_bfloat16* dst = A.o + (row * A.Hq + h) * D;
 #pragma unroll
           for (int ds = 0; ds < KS; ++ds) {
@@ -484,15 +555,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
       }
   };
 
-  // ---- tiles
+  // ---- tiles. The descriptor of tile `it` was written two iterations ago, before a __syncwarp;
+  // a new segment's q is fetched while its first tile is still on its way.
+  __syncwarp();
   int stage = 0, next_tile = static_cast<int>(ub - seg_begin);
   for (int it = 0; it < ntiles; ++it) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
     const int4 t = ring[warp][it & 3];
-    // the stage that was consumed in the last iteration takes the next tile
-    issue(stage == 0 ? kStages - 1 : stage - 1, (it + kStages - 1) & 3);
-    look_up();
     if (t.x != seg) {
       if (seg >= 0) {
         finish(seg, first_tile_of_seg, cur_tiles);
@@ -504,6 +572,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
       first_tile_of_seg = next_tile;
       begin(seg);
     }
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    // the stage that was consumed in the last iteration takes the next tile
+    issue(stage == 0 ? kStages - 1 : stage - 1, (it + kStages - 1) & 3);
+    look_up();
     ++next_tile;
     const int nk = t.z & 0xffff;
     bad |= (t.z >> 16) != 0;
@@ -516,24 +589,31 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         klim[nt][j] =
-            (!SPARSE || ((rows >> (nt * 8 + 2 * c + j)) & 1)) ? min(lim[nt][j], t.y + nk) : 0;
-#pragma unroll 1
-    for (int sub = 0; sub < KT / 32; ++sub) {
-      if (sub * 32 >= nk) break;
-      float sacc[2][NT][4];
+            lim[nt][j] == kNoLimit ? kNoLimit
+            : (!SPARSE || ((rows >> (nt * 8 + 2 * c + j)) & 1)) ? min(lim[nt][j], t.y + nk) : 0;
+    bool masked = false;  // a key of the tile is hidden from a row
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) masked |= klim[nt][j] < t.y + KT;
+    masked = __any_sync(0xffffffffu, masked);
+#pragma unroll 1
+    for (int sub = 0; sub < KT / SUB; ++sub) {
+      if (sub * SUB >= nk) break;
+      float sacc[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 4; ++x) sacc[mt][nt][x] = 0.f;
       // S^T = K Q^T
-      const int krow = sub * 32 + (lane & 15);
+      const int krow = sub * SUB + (lane & 15);
       if (!FP8) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
+          for (int mt = 0; mt < MT; ++mt) {
             uint32_t a[4];
             ldsm4(a, kb + swz<RB>(krow + mt * 16, ks * 2 + (lane >> 4)));
 #pragma unroll
@@ -544,17 +624,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
 #pragma unroll
         for (int k2 = 0; k2 < KS / 2; ++k2)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
+          for (int mt = 0; mt < MT; ++mt) {
             // matrices: (keys 0-7, 16 columns), (keys 8-15, same), then the next 16 columns
             uint32_t b[4];
             ldsm4(b, kb + swz<RB>(krow + mt * 16, k2 * 2 + (lane >> 4)));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t a[4];
-              a[0] = widen2(b[2 * h]);
-              a[1] = widen2(b[2 * h + 1]);
-              a[2] = widen2(b[2 * h] >> 16);
-              a[3] = widen2(b[2 * h + 1] >> 16);
+              a[0] = widen_lo(b[2 * h]);
+              a[1] = widen_lo(b[2 * h + 1]);
+              a[2] = widen_hi(b[2 * h]);
+              a[3] = widen_hi(b[2 * h + 1]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma16816<true>(sacc[mt][nt], a, qf[2 * k2 + h][nt][0], qf[2 * k2 + h][nt][1]);
@@ -562,70 +642,99 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
           }
       }
       // softmax: this lane holds keys n4 + 8 x of each 16, columns 2c, 2c + 1
-      float kmul[2][2];
-      int vexp[2][2];
+      float ve[MT][2];  // exponent of the value's scale
       if (FP8) {
-        int top = 0;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int key = sub * 32 + mt * 16 + x * 8 + n4;
-            kmul[mt][x] = __uint_as_float(static_cast<uint32_t>(sc[key]) << 23);
-            vexp[mt][x] = key < nk ? sc[KT + key] : 0;
-            top = max(top, vexp[mt][x]);
+            const int key = sub * SUB + mt * 16 + x * 8 + n4;
+            const float f = __uint_as_float(static_cast<uint32_t>(sc[key]) << 23);
+            ve[mt][x] = static_cast<float>(static_cast<int>(sc[KT + key]) - 127);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              sacc[mt][nt][2 * x] *= f;
+              sacc[mt][nt][2 * x + 1] *= f;
+            }
           }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (top > vref) {  // uniform: a larger value scale than all before
-          const int e = 127 + vref - top;
-          const float f = e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.f;
+      }
+      if (masked) {
 #pragma unroll
-          for (int ds = 0; ds < KS; ++ds)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) acc[ds][nt][x] *= f;
-          vref = top;
-        }
+            for (int x = 0; x < 4; ++x) {
+              const int key = t.y + sub * SUB + mt * 16 + (x >> 1) * 8 + n4;
+              if (key >= klim[nt][x & 1]) sacc[mt][nt][x] = -INFINITY;
+            }
       }
       float corr[NT][2];
       bool grew = false;
+      uint32_t pf[MT][NT][2];  // P^T as the second operand: 8 x 8 pieces turned within the warp
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[MT][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float best = -INFINITY;
+          const float cm = cmul[nt][j];
+          float best = -INFINITY, own = -INFINITY;
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const int key = t.y + sub * 32 + mt * 16 + x * 8 + n4;
-              float z = sacc[mt][nt][2 * x + j] * cmul[nt][j];
-              if (FP8) z *= kmul[mt][x];
-              z = key < klim[nt][j] ? z : -INFINITY;
-              sacc[mt][nt][2 * x + j] = z;
-              best = fmaxf(best, z);
+              const float z = sacc[mt][nt][2 * x + j];  // before the factor cm > 0
+              if (FP8) {
+                own = fmaxf(own, z);
+                w[mt][2 * x + j] = fmaf(z, cm, ve[mt][x]);
+                best = fmaxf(best, w[mt][2 * x + j]);
+              } else {
+                best = fmaxf(best, z);
+              }
             }
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1)
             best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+          if (!FP8) best *= cm;
           const float mn = fmaxf(m[nt][j], best);
-          corr[nt][j] = mn > m[nt][j] ? exp2f(m[nt][j] - mn) : 1.f;  // 0 for the first keys
+          corr[nt][j] = mn > m[nt][j] ? ex2(m[nt][j] - mn) : 1.f;  // 0 for the first keys
           grew |= mn > m[nt][j];
           m[nt][j] = mn;
-          // no key yet: any finite reference gives p = 0
-          const float ref = (mn == -INFINITY ? 0.f : mn) - (FP8 ? 15.f : 0.f);
+          // no key yet: any finite reference gives weights of 0
+          const float ref = mn == -INFINITY ? 0.f : mn;
           float sum = 0.f;
+          if (FP8) {
+            const float rn = fmaxf(r[nt][j], own * cm);
+            const float rref = rn == -INFINITY ? 0.f : rn;
+            const float keep = rn > r[nt][j] ? ex2(r[nt][j] - rn) : 1.f;
+            r[nt][j] = rn;
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float p = exp2f(sacc[mt][nt][2 * x + j] - ref);
-              sacc[mt][nt][2 * x + j] = p;
-              sum += p;
-            }
-          l[nt][j] = fmaf(l[nt][j], corr[nt][j], sum);
+              for (int x = 0; x < 2; ++x) {
+                sum += ex2(fmaf(sacc[mt][nt][2 * x + j], cm, -rref));
+                w[mt][2 * x + j] = ex2(w[mt][2 * x + j] - (ref - 15.f));
+              }
+            l[nt][j] = fmaf(l[nt][j], keep, sum);
+          } else {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float p = ex2(fmaf(sacc[mt][nt][2 * x + j], cm, -ref));
+                w[mt][2 * x + j] = p;
+                sum += p;
+              }
+            l[nt][j] = fmaf(l[nt][j], corr[nt][j], sum);
+          }
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            pf[mt][nt][x] = transpose8x8(FP8 ? pack_f16(w[mt][2 * x], w[mt][2 * x + 1])
+                                             : pack_bf16(w[mt][2 * x], w[mt][2 * x + 1]));
+      }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
         for (int ds = 0; ds < KS; ++ds)
@@ -634,32 +743,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc[ds][nt][x] *= corr[nt][x & 1];
       }
-      // P^T as the second operand: 8 x 8 pieces turned within the warp
-      uint32_t pf[2][NT][2];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float p0 = sacc[mt][nt][2 * x], p1 = sacc[mt][nt][2 * x + 1];
-            uint32_t u;
-            if (FP8) {
-              const int e = 127 + vexp[mt][x] - vref;
-              const float f = e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.f;
-              u = pack_f16(p0 * f, p1 * f);
-            } else {
-              u = pack_bf16(p0, p1);
-            }
-            pf[mt][nt][x] = transpose8x8(u);
-          }
       // O^T += V^T P^T
       if (!FP8) {
-        const int vrow = sub * 32 + ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+        const int vrow = sub * SUB + ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
 #pragma unroll
         for (int ds = 0; ds < KS; ++ds)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
+          for (int mt = 0; mt < MT; ++mt) {
             uint32_t a[4];
             ldsm4t(a, vb + swz<RB>(vrow + mt * 16, ds * 2 + half));
 #pragma unroll
@@ -669,11 +759,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
       } else {
         // matrices: (keys 0-7, 16 columns), (keys 8-15, same), then the next 16 columns; a
         // register holds columns 2i, 2i + 1 of keys 2c, 2c + 1
-        const int vrow = sub * 32 + (((lane >> 3) & 1) << 3) + (lane & 7);
+        const int vrow = sub * SUB + (((lane >> 3) & 1) << 3) + (lane & 7);
 #pragma unroll
         for (int d2 = 0; d2 < KS / 2; ++d2)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
+          for (int mt = 0; mt < MT; ++mt) {
             uint32_t b[4];
             ldsm4t(b, vb + swz<RB>(vrow + mt * 16, d2 * 2 + (lane >> 4)));
 #pragma unroll
@@ -681,10 +771,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
               const uint32_t lo = __byte_perm(b[2 * h], 0, 0x3120);
               const uint32_t hi = __byte_perm(b[2 * h + 1], 0, 0x3120);
               uint32_t a[4];
-              a[0] = widen2(lo);        // column 2i of keys 2c, 2c + 1
-              a[1] = widen2(lo >> 16);  // column 2i + 1
-              a[2] = widen2(hi);        // keys 8 + 2c, 8 + 2c + 1
-              a[3] = widen2(hi >> 16);
+              a[0] = widen_lo(lo);  // column 2i of keys 2c, 2c + 1
+              a[1] = widen_hi(lo);  // column 2i + 1
+              a[2] = widen_lo(hi);  // keys 8 + 2c, 8 + 2c + 1
+              a[3] = widen_hi(hi);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma16816<true>(acc[2 * d2 + h][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
@@ -699,55 +789,70 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const Page
 }
 
 // ------------------------------------------------------------------------------------- merge
-// One CTA per (sequence, row, head): the partials of its segment, four warps taking every fourth,
-// joined in a fixed order. Rows without keys get o = 0, lse = -inf; a row whose sequence names a
-// page outside the pool gets NaN.
+// One CTA per (sequence, row, head): the partials of its segment, its warps taking every NW-th,
+// joined in a fixed order. Bound by latency: two dependent loads (the segment's description, then
+// the partials), so a warp has kMergeBatch partials in flight at once and the host gives a CTA
+// more warps the fewer segments share the partials. Rows without keys get o = 0, lse = -inf; a
+// row whose sequence names a page outside the pool gets NaN.
+constexpr int kMergeBatch = 8;
+constexpr int kMergeWarps = 8;  // at most
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs A, int kRows,
-                                                          bool sparse) {
-  __shared__ float sm[4], sl[4], so[4][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedArgs A,
+                                                                       int kRows, bool sparse) {
+  __shared__ float sm[kMergeWarps], sl[kMergeWarps], so[kMergeWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, NW = blockDim.x >> 5;
   constexpr int PER = D / 32;
   const int h = blockIdx.x % A.Hq, row = blockIdx.x / A.Hq;
   const int s = row / A.rows, r = row % A.rows, g = h / A.group;
   const int rr = r * A.group + h % A.group, rt = rr / kRows, col = rr % kRows;
   const int seg = (s * A.G + g) * A.nrt + rt;
-  wait_previous_kernel();
   bool over;
   const int L = seq_len(A, s, &over);
-  int count = 0, first = 0;
-  bool bad = over;
-  if (sparse) {
-    const int tiles = A.seg_tiles[seg];
-    bad |= tiles < 0;
-    if (tiles > 0) count = A.seg_count[seg];
-  } else if (L > 0) {
-    count = A.seg_count[seg];
-  }
+  wait_previous_kernel();
+  // written for every segment that has tiles
+  const int2 desc = A.seg_desc[seg];
+  const int tiles = sparse ? A.seg_tiles[seg] : L;
+  const int count = tiles > 0 ? desc.y : 0;
+  bool bad = over || tiles < 0;
   if (count == 1) return;  // written by the warp that had all of it
-  if (count) first = A.seg_first[seg];
   float m = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  const size_t slot0 = static_cast<size_t>(first) + seg;
-#pragma unroll 4
-  for (int i = warp; i < count; i += 4) {
-    const size_t at = (slot0 + i) * kRows + col;
-    const float2 ml = A.part_ml[at];
-    float o[PER];
+  const size_t slot0 = static_cast<size_t>(desc.x) + seg;
+  for (int i0 = warp; i0 < count; i0 += NW * kMergeBatch) {
+    float2 ml[kMergeBatch];
+    float o[kMergeBatch][PER];
 #pragma unroll
-    for (int e = 0; e < PER; e += 2) {
-      const float2 f = *reinterpret_cast<const float2*>(A.part_o + at * D + lane * PER + e);
-      o[e] = f.x;
-      o[e + 1] = f.y;
+    for (int x = 0; x < kMergeBatch; ++x) {
+      const int i = i0 + x * NW;
+      ml[x] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[x][e] = 0.f;
+      if (i < count) {
+        const size_t at = (slot0 + i) * kRows + col;
+        ml[x] = A.part_ml[at];
+        const float* src = A.part_o + at * D + lane * PER;
+        if constexpr (PER == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          o[x][0] = f.x; o[x][1] = f.y; o[x][2] = f.z; o[x][3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          o[x][0] = f.x; o[x][1] = f.y;
+        }
+      }
     }
-    if (!(ml.x <= FLT_MAX)) { bad = true; continue; }  // NaN: a bad page
-    if (!(ml.y > 0.f)) continue;
-    const float mn = fmaxf(m, ml.x), a = exp2f(m - mn), b = exp2f(ml.x - mn) * ml.y;
-    l = fmaf(l, a, b);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = fmaf(acc[e], a, b * o[e]);
-    m = mn;
+    for (int x = 0; x < kMergeBatch; ++x) {
+      bad |= !(ml[x].x <= FLT_MAX);  // NaN: a bad page
+      if (ml[x].y > 0.f) {
+        const float mn = fmaxf(m, ml[x].x), a = exp2f(m - mn), b = exp2f(ml[x].x - mn) * ml[x].y;
+        l = fmaf(l, a, b);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(acc[e], a, b * o[x][e]);
+        m = mn;
+      }
+    }
   }
   if (lane == 0) {
     sm[warp] = bad ? __int_as_float(0x7fffffff) : m;
@@ -758,23 +863,18 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs A, int
   __syncthreads();
   float M = -INFINITY, Lsum = 0.f;
   bool any_bad = false;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < NW; ++w) {
     any_bad |= sm[w] != sm[w];
     M = fmaxf(M, sm[w]);
   }
-  float wt[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    wt[w] = sl[w] > 0.f ? exp2f(sm[w] - M) : 0.f;
-    Lsum = fmaf(wt[w], sl[w], Lsum);
-  }
+  for (int w = 0; w < NW; ++w)
+    if (sl[w] > 0.f) Lsum = fmaf(exp2f(sm[w] - M), sl[w], Lsum);
   const float inv = any_bad ? __int_as_float(0x7fffffff) : Lsum > 0.f ? 1.f / Lsum : 0.f;
-  if (threadIdx.x < D) {
+  for (int x = threadIdx.x; x < D; x += blockDim.x) {
     float o = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) o = fmaf(wt[w], so[w][threadIdx.x], o);
-    A.o[(static_cast<size_t>(row) * A.Hq + h) * D + threadIdx.x] = __float2bfloat16_rn(o * inv);
+    for (int w = 0; w < NW; ++w)
+      if (sl[w] > 0.f) o = fmaf(exp2f(sm[w] - M), so[w][x], o);
+    A.o[(static_cast<size_t>(row) * A.Hq + h) * D + x] = __float2bfloat16_rn(o * inv);
   }
   if (threadIdx.x == 0)
     A.lse[static_cast<size_t>(h) * A.nseq * A.rows + row] =
@@ -788,13 +888,20 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs A, int
 // Scores are q . (block sum): the mean's 1 / B is common to the past blocks, which are all full.
 // They are accumulated in fp64 (products of bf16 and fp32 are exact there), so the selection does
 // not hang on the order of the sum; fp64 runs at half the fp32 rate here and the scores are a
-// small part of the step. One cluster per segment: its CTAs score every CS-th run of 32 blocks
-// (lanes over blocks, the 8 warps over eighths of d, so a sum is widened to fp64 once for all
-// rows), then each row's selection is one warp's: a radix selection on order-preserving 64-bit
-// keys whose 256 bins span only the range still in question (usually two or three sweeps).
-// Equal scores: the lower block first.
+// small part of the step. Equal scores: the lower block first.
+//
+// Bound by latency (a chain of page id, sum, score, selection, list), so: one cluster of up to 8
+// CTAs per segment, eight lanes to a block's sum so that a CTA of 8 warps has 32 blocks in flight;
+// the page ids and q are fetched before the sequence's length is known; all rows' partial sums of
+// a block are reduced together, a lane keeping half of its values at each step; and the selection is
+// ranking by 32 shuffles (at most 32 past blocks), one warp per row with its keys in registers (at
+// most 256), or one CTA per row (beyond; keys in registers up to 2048). The latter two are a radix selection on
+// order-preserving 64-bit keys whose 256 bins span only the range still in question: usually two
+// or three sweeps instead of the eight that fixed bytes of an fp64 key would take.
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
+constexpr int kGateInRegs = 8;  // keys a thread holds in a selection
+constexpr int kGateWords = kMaxBlocksPerSeq / 32;
 
 __device__ __forceinline__ unsigned long long order_key64(double x) {
   if (x != x) return 0ull;  // NaN: behind every number
@@ -803,18 +910,91 @@ __device__ __forceinline__ unsigned long long order_key64(double x) {
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
+// Sum over groups of eight lanes of each of RR values per lane. At each step a lane keeps half of
+// its values and hands over the other half, so lane x of a group ends with the sums of values
+// first(x) .. first(x) + max(1, RR / 8) - 1 in v[0] ..., and RR < 8 leaves 8 / RR lanes with the same.
+template <int RR>
+__device__ __forceinline__ void reduce_rows8(double (&v)[RR], int lane) {
+  int n = RR;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    if (n > 1) {
+      const bool up = lane & o;
+      n >>= 1;
+#pragma unroll
+      for (int i = 0; i < RR / 2; ++i)
+        if (i < n) {
+          const double give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+}
+
+// One bin of a radix pass: the highest bin that brings the count from the top to `want`.
+// Returns the bin, the keys in it and the keys above it; every lane of the warp gets them.
+__device__ __forceinline__ void pick_bin(const int* hist, int want, int lane, int* bin, int* cnt,
+                                         int* above) {
+  int bins[8], mine = 0;  // lane 0 has the eight highest bins
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    bins[x] = hist[255 - (lane * 8 + x)];
+    mine += bins[x];
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
+  int ab = incl - mine, b = 0, c = 0;
+#pragma unroll
+  for (int x = 0; x < 8; ++x)
+    if (c == 0) {
+      if (ab + bins[x] >= want) { b = 255 - (lane * 8 + x); c = bins[x]; }
+      else ab += bins[x];
+    }
+  *bin = __shfl_sync(0xffffffffu, b, src);
+  *cnt = __shfl_sync(0xffffffffu, c, src);
+  *above = __shfl_sync(0xffffffffu, ab, src);
+}
+
+// State of a radix selection of the `want` largest keys: keys above thr are in, and the first
+// need_eq (lowest blocks) of those equal to it.
+struct Radix {
+  unsigned long long thr, range;
+  int want, need_eq;
+  __device__ __forceinline__ int shift() const {
+    return max(0, 56 - __clzll(static_cast<long long>(range)));
+  }
+  // Narrows to the picked bin; true when the selection is settled.
+  __device__ __forceinline__ bool narrow(int bin, int cnt, int above) {
+    const int sh = shift();
+    const unsigned long long step = static_cast<unsigned long long>(bin) << sh;
+    want -= above;
+    thr += step;
+    if (cnt == want) { need_eq = 0x7fffffff; return true; }  // the whole bin
+    if (sh == 0) { need_eq = want; return true; }            // one key value
+    range = min(range - step, (1ull << sh) - 1);
+    return false;
+  }
+};
+
 template <int D, int RR>
-__global__ void __launch_bounds__(kGateThreads) paged_gate_kernel(const PagedArgs A, int kRows,
+__global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const PagedArgs A, int kRows,
                                                                   int KT, int in_smem) {
-  constexpr int CP = D + 4;        // padded row of the staged sums
-  constexpr int SL = D / kGateWarps;  // columns of d per warp
+  constexpr int NV = D / 32;  // 16-byte pieces of a sum per lane (eight lanes have a block)
+  constexpr int U = RR >= 8 ? 1 : RR >= 4 || D == 128 ? 2 : 4;  // blocks in flight per eight lanes
   extern __shared__ __align__(1024) uint8_t smem[];
-  double* qd = reinterpret_cast<double*>(smem);               // [RR][D]
-  double* red = qd + RR * D;                                  // [8][RR][32]
-  float* cs = reinterpret_cast<float*>(red + kGateWarps * RR * 32);  // [32][CP]
-  int* hist = reinterpret_cast<int*>(cs + 32 * CP);           // [8][256]
-  unsigned long long* skeys = reinterpret_cast<unsigned long long*>(hist + kGateWarps * 256);
+  unsigned long long* skeys = reinterpret_cast<unsigned long long*>(smem);  // [RR][nb_cap]
+  __shared__ double qd[RR][D];
+  __shared__ int hist[kGateWarps][256];
+  __shared__ unsigned int bits[2][kGateWords];
   __shared__ int sbad, scan[kGateWarps], stot;
+  __shared__ unsigned long long slo[kGateWarps], shi[kGateWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
@@ -824,6 +1004,24 @@ __global__ void __launch_bounds__(kGateThreads) paged_gate_kernel(const PagedArg
   const Seg id = seg_of(A, seg);
   const int R = A.rows * A.group, row0 = id.rt * kRows;
   const int nrow = min(kRows, R - row0);  // rows of this tile (<= RR)
+  const int32_t* pages = A.page_table + static_cast<size_t>(id.s) * A.max_pages;
+  // eight lanes per block: this group's blocks are first, first + stride, ...
+  const int first = (rank * kGateWarps + warp) * 4 + (lane >> 3), stride = CS * kGateWarps * 4;
+  auto page_of = [&](int j) {
+    return j < A.nb_cap ? __ldg(pages + ((static_cast<long long>(j) * A.B) >> A.page_log)) : -1;
+  };
+  int pid[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) pid[u] = A.topk > 1 ? page_of(first + u * stride) : -1;
+  for (int r = warp; r < RR; r += kGateWarps) {  // q as fp64
+    const int rr = row0 + r;
+    const __nv_bfloat16* src =
+        A.q + ((static_cast<size_t>(id.s) * A.rows + rr / A.group) * A.Hq +
+               static_cast<size_t>(id.g) * A.group + rr % A.group) * D;
+#pragma unroll
+    for (int x = lane; x < D; x += 32)
+      qd[r][x] = r < nrow ? static_cast<double>(__bfloat162float(src[x])) : 0.;
+  }
   bool over;
   const int L = seq_len(A, id.s, &over);
   const int last = L > 0 ? (L - 1) / A.B : -1;  // current block of the newest row
@@ -831,192 +1029,301 @@ __global__ void __launch_bounds__(kGateThreads) paged_gate_kernel(const PagedArg
       in_smem ? skeys : A.keys + static_cast<size_t>(seg) * kRows * A.nb_cap;
   unsigned int* marks = in_smem ? reinterpret_cast<unsigned int*>(skeys + RR * A.nb_cap)
                                 : A.marks + static_cast<size_t>(seg) * A.nb_cap;
-  const int32_t* pages = A.page_table + static_cast<size_t>(id.s) * A.max_pages;
   if (tid == 0) sbad = 0;
-  for (int j = rank * kGateThreads + tid; j <= last; j += CS * kGateThreads) marks[j] = 0;
+  if (RR > 1)
+    for (int j = rank * kGateThreads + tid; j <= last; j += CS * kGateThreads) marks[j] = 0;
   const bool scored = A.topk > 1 && A.topk - 1 < last;
   if (scored) {
-    for (int x = tid; x < RR * D; x += kGateThreads) {
-      const int rr = row0 + x / D;
-      double v = 0.;
-      if (x / D < nrow)
-        v = static_cast<double>(__bfloat162float(
-            A.q[((static_cast<size_t>(id.s) * A.rows + rr / A.group) * A.Hq +
-                 static_cast<size_t>(id.g) * A.group + rr % A.group) * D + x % D]));
-      qd[x] = v;
-    }
-    for (int j0 = rank * 32; j0 < last; j0 += CS * 32) {
-      __syncthreads();
-      for (int x = tid; x < 32 * (D / 4); x += kGateThreads) {
-        const int j = x / (D / 4), cc = x % (D / 4);
-        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j0 + j < last) {
-          const int pid =
-              __ldg(pages + ((static_cast<long long>(j0 + j) * A.B) >> A.page_log));
-          if (pid >= 0 && pid < A.num_pages)
-            f = __ldg(reinterpret_cast<const float4*>(
-                          A.sums + (static_cast<size_t>(pid) * A.G + id.g) * D) + cc);
-          else
-            sbad = 1;
+    __syncthreads();
+    const int l8 = lane & 7;
+    // the warp's four blocks are neighbours: all its lanes leave the loop together
+    for (int j0 = first; j0 - (lane >> 3) < last; j0 += U * stride) {
+      float4 c[U][NV];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = j0 + u * stride < last, ok = pid[u] >= 0 && pid[u] < A.num_pages;
+        const float4* src = reinterpret_cast<const float4*>(
+            A.sums + (static_cast<size_t>(ok ? pid[u] : 0) * A.G + id.g) * D);
+#pragma unroll
+        for (int x = 0; x < NV; ++x)
+          c[u][x] = in && ok ? __ldg(src + l8 + 8 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in && !ok) sbad = 1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) pid[u] = page_of(j0 + (U + u) * stride);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * stride;
+        if (j - (lane >> 3) >= last) break;  // uniform over the warp
+        double v[RR];
+#pragma unroll
+        for (int r = 0; r < RR; ++r) v[r] = 0.;
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+          const double cd[4] = {c[u][x].x, c[u][x].y, c[u][x].z, c[u][x].w};
+#pragma unroll
+          for (int r = 0; r < RR; ++r) {
+            const double2* qp = reinterpret_cast<const double2*>(&qd[r][(l8 + 8 * x) * 4]);
+            const double2 a = qp[0], b = qp[1];
+            v[r] = fma(a.x, cd[0], v[r]);
+            v[r] = fma(a.y, cd[1], v[r]);
+            v[r] = fma(b.x, cd[2], v[r]);
+            v[r] = fma(b.y, cd[3], v[r]);
+          }
         }
-        *reinterpret_cast<float4*>(cs + j * CP + cc * 4) = f;
-      }
-      __syncthreads();
-      double acc[RR];
+        reduce_rows8<RR>(v, lane);
+        if (j < last) {
+          if constexpr (RR >= 8) {
 #pragma unroll
-      for (int r = 0; r < RR; ++r) acc[r] = 0.;
-#pragma unroll
-      for (int x = 0; x < SL; x += 4) {
-        const int col = warp * SL + x;
-        const float4 f = *reinterpret_cast<const float4*>(cs + lane * CP + col);
-        const double c[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int r = 0; r < RR; ++r) acc[r] = fma(qd[r * D + col + e], c[e], acc[r]);
-      }
-#pragma unroll
-      for (int r = 0; r < RR; ++r) red[(warp * RR + r) * 32 + lane] = acc[r];
-      __syncthreads();
-      for (int x = tid; x < RR * 32; x += kGateThreads) {
-        const int r = x >> 5, j = j0 + (x & 31);
-        double v = 0.;
-#pragma unroll
-        for (int w = 0; w < kGateWarps; ++w) v += red[(w * RR + r) * 32 + (x & 31)];
-        if (r < nrow && j < last) keys[static_cast<size_t>(r) * A.nb_cap + j] = order_key64(v);
+            for (int i = 0; i < RR / 8; ++i) {
+              const int r = l8 * (RR / 8) + i;
+              if (r < nrow) keys[static_cast<size_t>(r) * A.nb_cap + j] = order_key64(v[i]);
+            }
+          } else {
+            const int r = l8 / (8 / RR);
+            if (l8 % (8 / RR) == 0 && r < nrow)
+              keys[static_cast<size_t>(r) * A.nb_cap + j] = order_key64(v[0]);
+          }
+        }
       }
     }
   }
   cluster.sync();
-  // ---- selection: row r of the tile by warp (r / CS) of rank r % CS
-  for (int r = rank + CS * warp; r < nrow; r += CS * kGateWarps) {
+
+  // ---- selection. select(row, where) writes its results through these.
+  int2* ent = A.entries + static_cast<size_t>(seg) * A.ent_cap;
+  auto place = [&](int r, int* pos_block) -> int32_t* {  // row's output, and its current block
     const int rr = row0 + r, tok = rr / A.group, h = id.g * A.group + rr % A.group;
     const int pos = L - A.rows + tok;
-    int32_t* out = A.idx ? A.idx + (static_cast<size_t>(h) * A.nseq * A.rows +
-                                    static_cast<size_t>(id.s) * A.rows + tok) * A.topk
-                         : nullptr;
-    const int i = pos >= 0 ? pos / A.B : -1;  // past blocks, and the current one
-    const int want = min(A.topk - 1, max(i, 0));
-    const unsigned int bit = 1u << r;
-    if (i >= 0 && !over) {
-      const unsigned long long* kr = keys + static_cast<size_t>(r) * A.nb_cap;
-      unsigned long long thr = 0;
-      int need_eq = 0x7fffffff;
+    *pos_block = pos >= 0 && !over ? pos / A.B : -1;
+    return A.idx ? A.idx + (static_cast<size_t>(h) * A.nseq * A.rows +
+                            static_cast<size_t>(id.s) * A.rows + tok) * A.topk
+                 : nullptr;
+  };
+  auto take = [&](int32_t* out, int r, int at, int j) {
+    if (out) out[at] = j;
+    if (RR > 1) atomicOr(marks + j, 1u << r);
+    else ent[at] = make_int2(j, 1);
+  };
+  if (last <= 32 * kGateInRegs) {
+    // row r by warp r / CS of rank r % CS
+    for (int r = rank + CS * warp; r < nrow; r += CS * kGateWarps) {
+      int i;
+      int32_t* out = place(r, &i);
+      const int want = min(A.topk - 1, max(i, 0));
+      unsigned long long kk[kGateInRegs];
+      Radix S{0ull, 0ull, want, 0x7fffffff};
+      bool ranked = false, in32 = false;
       if (want > 0 && want < i) {
-        unsigned long long base = ~0ull, top = 0;
-#pragma unroll 4
-        for (int j = lane; j < i; j += 32) {
-          base = min(base, kr[j]);
-          top = max(top, kr[j]);
-        }
+        const unsigned long long* kr = keys + static_cast<size_t>(r) * A.nb_cap;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          base = min(base, __shfl_xor_sync(0xffffffffu, base, o));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        }
-        unsigned long long range = top - base;
-        int w = want;
-        int* hs = hist + warp * 256;
-        while (true) {
-          if (range == 0) {
-            need_eq = w;
-            break;
+        for (int x = 0; x < kGateInRegs; ++x)
+          kk[x] = x * 32 + lane < i ? kr[x * 32 + lane] : 0ull;
+        if (i <= 32) {
+          int rank32 = 0;  // keys before this lane's in the order of selection
+          for (int x = 0; x < i; ++x) {
+            const unsigned long long k = __shfl_sync(0xffffffffu, kk[0], x);
+            rank32 += k > kk[0] || (k == kk[0] && x < lane);
           }
-          const int shift = max(0, 56 - __clzll(static_cast<long long>(range)));
+          ranked = true;
+          in32 = rank32 < want;
+        } else {
+          unsigned long long lo = ~0ull, hi = 0;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) hs[x * 32 + lane] = 0;
-          __syncwarp();
-#pragma unroll 4
-          for (int j = lane; j < i; j += 32) {
-            const unsigned long long d = kr[j] - base;  // wraps above range for smaller keys
-            if (d <= range) atomicAdd(&hs[static_cast<int>(d >> shift)], 1);
-          }
-          __syncwarp();
-          int bins[8], mine = 0;  // lane 0 has the eight highest bins
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            bins[x] = hs[255 - (lane * 8 + x)];
-            mine += bins[x];
-          }
-          int incl = mine;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          const int src = __ffs(__ballot_sync(0xffffffffu, incl >= w)) - 1;
-          int above = incl - mine, bin = 0, cnt = 0;
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            if (cnt == 0) {
-              if (above + bins[x] >= w) { bin = 255 - (lane * 8 + x); cnt = bins[x]; }
-              else above += bins[x];
+          for (int x = 0; x < kGateInRegs; ++x)
+            if (x * 32 + lane < i) {
+              lo = min(lo, kk[x]);
+              hi = max(hi, kk[x]);
             }
-          bin = __shfl_sync(0xffffffffu, bin, src);
-          cnt = __shfl_sync(0xffffffffu, cnt, src);
-          above = __shfl_sync(0xffffffffu, above, src);
-          w -= above;
-          const unsigned long long step = static_cast<unsigned long long>(bin) << shift;
-          base += step;
-          if (cnt == w) break;  // the whole bin
-          if (shift == 0) {     // one key value: the lowest blocks of it
-            need_eq = w;
-            break;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
           }
-          range = min(range - step, (1ull << shift) - 1);
-          __syncwarp();
+          S.thr = lo;
+          S.range = hi - lo;
+          S.need_eq = want;
+          if (S.range)
+            while (true) {
+              const int sh = S.shift();
+#pragma unroll
+              for (int x = 0; x < 8; ++x) hist[warp][x * 32 + lane] = 0;
+              __syncwarp();
+#pragma unroll
+              for (int x = 0; x < kGateInRegs; ++x) {
+                const unsigned long long d = kk[x] - S.thr;  // wraps above range for lower keys
+                if (x * 32 + lane < i && d <= S.range)
+                  atomicAdd(&hist[warp][static_cast<int>(d >> sh)], 1);
+              }
+              __syncwarp();
+              int bin, cnt, above;
+              pick_bin(hist[warp], S.want, lane, &bin, &cnt, &above);
+              if (S.narrow(bin, cnt, above)) break;
+              __syncwarp();
+            }
         }
-        thr = base;
       }
       int at = 0, eq = 0;
-      if (want > 0)
-        for (int j0 = 0; j0 < i; j0 += 32) {
-          const int j = j0 + lane;
-          const unsigned long long k = want < i && j < i ? kr[j] : 0ull;
-          const bool same = j < i && want < i && k == thr;
-          const unsigned eqs = __ballot_sync(0xffffffffu, same);
-          bool sel = j < i && (want == i || k > thr);
-          if (same) sel = eq + __popc(eqs & ((1u << lane) - 1)) < need_eq;
-          const unsigned sels = __ballot_sync(0xffffffffu, sel);
-          if (sel) {
-            if (out) out[at + __popc(sels & ((1u << lane) - 1))] = j;
-            atomicOr(marks + j, bit);
+      if (want > 0) {
+#pragma unroll
+        for (int x = 0; x < kGateInRegs; ++x) {
+          const int j = x * 32 + lane;
+          if (x * 32 >= i) break;
+          bool sel = j < i && (want == i || (ranked ? in32 : kk[x] > S.thr));
+          if (want < i && !ranked) {
+            const bool same = j < i && kk[x] == S.thr;
+            const unsigned eqs = __ballot_sync(0xffffffffu, same);
+            if (same) sel = eq + __popc(eqs & ((1u << lane) - 1)) < S.need_eq;
+            eq += __popc(eqs);
           }
+          const unsigned sels = __ballot_sync(0xffffffffu, sel);
+          if (sel) take(out, r, at + __popc(sels & ((1u << lane) - 1)), j);
           at += __popc(sels);
-          eq += __popc(eqs);
         }
-      if (lane == 0) {
-        if (out) out[want] = i;
-        atomicOr(marks + i, bit);
       }
+      if (i >= 0 && lane == 0) take(out, r, want, i);
+      if (out)
+        for (int x = (i >= 0 ? want + 1 : 0) + lane; x < A.topk; x += 32) out[x] = -1;
+      if (RR == 1 && lane == 0) stot = i >= 0 ? want + 1 : 0;
     }
-    if (out)
-      for (int x = (i >= 0 && !over ? want + 1 : 0) + lane; x < A.topk; x += 32) out[x] = -1;
+  } else {
+    for (int r = rank; r < nrow; r += CS) {  // uniform over the CTA
+      int i;
+      int32_t* out = place(r, &i);
+      const int want = min(A.topk - 1, max(i, 0));
+      if (want > 0) {  // want < i here: i is near `last`, far above the largest topk
+        const unsigned long long* kr = keys + static_cast<size_t>(r) * A.nb_cap;
+        const bool in_regs = i <= kGateThreads * kGateInRegs;
+        unsigned long long kk[kGateInRegs];
+        if (in_regs) {
+#pragma unroll
+          for (int x = 0; x < kGateInRegs; ++x)
+            kk[x] = x * kGateThreads + tid < i ? kr[x * kGateThreads + tid] : 0ull;
+        }
+        // f(j, key) for this thread's blocks tid, tid + 256, ...
+        auto each = [&](auto f) {
+          if (in_regs) {
+#pragma unroll
+            for (int x = 0; x < kGateInRegs; ++x)
+              if (x * kGateThreads + tid < i) f(x * kGateThreads + tid, kk[x]);
+          } else {
+#pragma unroll 8
+            for (int j = tid; j < i; j += kGateThreads) f(j, kr[j]);
+          }
+        };
+        unsigned long long lo = ~0ull, hi = 0;
+        each([&](int, unsigned long long k) {
+          lo = min(lo, k);
+          hi = max(hi, k);
+        });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        if (lane == 0) {
+          slo[warp] = lo;
+          shi[warp] = hi;
+        }
+        hist[0][tid] = 0;
+        __syncthreads();
+        for (int w = 0; w < kGateWarps; ++w) {
+          lo = min(lo, slo[w]);
+          hi = max(hi, shi[w]);
+        }
+        Radix S{lo, hi - lo, want, want};
+        if (S.range)
+          while (true) {
+            const int sh = S.shift();
+            each([&](int, unsigned long long k) {
+              const unsigned long long d = k - S.thr;  // wraps above range for lower keys
+              if (d <= S.range) atomicAdd(&hist[0][static_cast<int>(d >> sh)], 1);
+            });
+            __syncthreads();
+            int bin, cnt, above;
+            pick_bin(hist[0], S.want, lane, &bin, &cnt, &above);  // every warp alike
+            __syncthreads();
+            if (S.narrow(bin, cnt, above)) break;
+            hist[0][tid] = 0;
+            __syncthreads();
+          }
+        // selected blocks as bits, 32 blocks to a word
+        const bool all_eq = S.need_eq == 0x7fffffff;
+        for (int x = tid; x < 2 * kGateWords; x += kGateThreads) (&bits[0][0])[x] = 0;
+        __syncthreads();
+        each([&](int j, unsigned long long k) {
+          if (k > S.thr || (all_eq && k == S.thr)) atomicOr(&bits[0][j >> 5], 1u << (j & 31));
+          else if (k == S.thr) atomicOr(&bits[1][j >> 5], 1u << (j & 31));
+        });
+        __syncthreads();
+        if (!all_eq && tid == 0) {  // several blocks of the border's score: the lowest ones
+          int left = S.need_eq;
+          for (int w = 0; left > 0; ++w) {
+            unsigned e = bits[1][w];
+            while (e && left > 0) {
+              bits[0][w] |= e & (0u - e);
+              e &= e - 1;
+              --left;
+            }
+          }
+        }
+        __syncthreads();
+        // thread t emits words 4t .. 4t + 3
+        int mine = 0;
+#pragma unroll
+        for (int w = 0; w < kGateWords / kGateThreads; ++w)
+          mine += __popc(bits[0][tid * (kGateWords / kGateThreads) + w]);
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        int at = incl - mine;
+        for (int w = 0; w < warp; ++w) at += scan[w];
+#pragma unroll
+        for (int w = 0; w < kGateWords / kGateThreads; ++w) {
+          const int word = tid * (kGateWords / kGateThreads) + w;
+          for (unsigned e = bits[0][word]; e; e &= e - 1) take(out, r, at++, word * 32 + __ffs(e) - 1);
+        }
+      }
+      if (i >= 0 && tid == 0) take(out, r, want, i);
+      if (out)
+        for (int x = (i >= 0 ? want + 1 : 0) + tid; x < A.topk; x += kGateThreads) out[x] = -1;
+      if (RR == 1 && tid == 0) stot = i >= 0 ? want + 1 : 0;
+      __syncthreads();  // shared arrays before the next row
+    }
   }
-  cluster.sync();
+  if (RR > 1) cluster.sync();  // all rows' marks
+  else __syncthreads();        // stot (rank 0 has the one row)
   if (rank == 0) {  // the blocks that a row selected, ascending
     bool bad = over;
     for (int r = 0; r < CS; ++r) bad |= *cluster.map_shared_rank(&sbad, r) != 0;
-    int2* ent = A.entries + static_cast<size_t>(seg) * A.ent_cap;
     int total = 0, has_last = 0;
-    for (int j0 = 0; j0 <= last; j0 += kGateThreads) {
-      const int j = j0 + tid;
-      const unsigned int mk = j <= last ? marks[j] : 0u;
-      const unsigned b = __ballot_sync(0xffffffffu, mk != 0);
-      if (lane == 0) scan[warp] = __popc(b);
-      __syncthreads();
-      int before = total, all = 0;
+    if (RR == 1) {
+      total = last >= 0 ? stot : 0;
+      has_last = total > 0;  // the one row is the newest
+    } else {
+      for (int j0 = 0; j0 <= last; j0 += kGateThreads) {
+        const int j = j0 + tid;
+        const unsigned int mk = j <= last ? marks[j] : 0u;
+        const unsigned b = __ballot_sync(0xffffffffu, mk != 0);
+        if (lane == 0) scan[warp] = __popc(b);
+        if (j == last) stot = mk != 0;
+        __syncthreads();
+        int before = total;
 #pragma unroll
-      for (int w = 0; w < kGateWarps; ++w) {
-        before += w < warp ? scan[w] : 0;
-        all += scan[w];
+        for (int w = 0; w < kGateWarps; ++w) {
+          before += w < warp ? scan[w] : 0;
+          total += scan[w];
+        }
+        if (mk) ent[before + __popc(b & ((1u << lane) - 1))] = make_int2(j, static_cast<int>(mk));
+        __syncthreads();
       }
-      if (mk) ent[before + __popc(b & ((1u << lane) - 1))] = make_int2(j, static_cast<int>(mk));
-      if (j == last) stot = mk != 0;
-      total += all;
-      __syncthreads();
+      if (last >= 0) has_last = stot;
     }
-    if (last >= 0) has_last = stot;
     if (tid == 0) {
       const int tail = L - max(last, 0) * A.B;
       A.seg_tiles[seg] = bad ? -1
@@ -1024,7 +1331,7 @@ __global__ void __launch_bounds__(kGateThreads) paged_gate_kernel(const PagedArg
                                    (has_last ? (tail + KT - 1) / KT : 0);
     }
   }
-  cluster.sync();  // peers' flags stay until rank 0 has read them
+  if (CS > 1) cluster.sync();  // peers' flags stay until rank 0 has read them
 }
 
 // -------------------------------------------------------------------------------------- host
@@ -1041,10 +1348,10 @@ PagedArgs args_of(const PagedLaunch& L) {
   A.rows = L.rows; A.Hq = L.Hq; A.group = L.Hq / P.G;
   A.nrt = L.shape.nrt; A.nseg = L.shape.nseg;
   A.topk = L.topk; A.nb_cap = L.shape.nb_cap; A.ent_cap = L.shape.ent_cap;
-  const int kt = kTileBytes / (P.d * (P.fp8 ? 1 : 2));
+  const int kt = tile_bytes(P.fp8) / (P.d * (P.fp8 ? 1 : 2));
   A.tiles_per_block = L.topk ? (P.B + kt - 1) / kt : 0;
   A.scale_log2 = L.scale * 1.4426950408889634f;
-  A.seg_first = L.seg_first; A.seg_count = L.seg_count;
+  A.seg_desc = reinterpret_cast<int2*>(L.seg_desc);
   A.part_o = L.part_o; A.part_ml = reinterpret_cast<float2*>(L.part_ml);
   A.seg_tiles = L.seg_tiles; A.entries = reinterpret_cast<int2*>(L.entries);
   A.keys = L.keys; A.marks = L.marks;
@@ -1070,12 +1377,12 @@ cudaError_t allow_smem(K kernel, int bytes, int (&done)[64]) {
 template <int D, bool FP8, int NT, bool SPARSE>
 cudaError_t attn(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
   static int done[64];
-  constexpr int smem = kPagedWarps * Tile<D, FP8>::kWarpBytes;
+  constexpr int smem = Tile<D, FP8>::kWarps * Tile<D, FP8>::kWarpBytes;
   cudaError_t e = allow_smem(paged_attn_kernel<D, FP8, NT, SPARSE>, smem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(L.shape.ctas));
-  cfg.blockDim = dim3(kPagedThreads);
+  cfg.blockDim = dim3(Tile<D, FP8>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -1089,9 +1396,8 @@ cudaError_t attn(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
 template <int D, int RR>
 cudaError_t gate(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
   static int done[64];
-  size_t smem = RR * D * 8 + kGateWarps * RR * 32 * 8 + 32 * (D + 4) * 4 + kGateWarps * 256 * 4;
-  const int in_smem = L.shape.gate_ctas == 1 && !L.shape.gate_global;
-  if (in_smem) smem += static_cast<size_t>(A.nb_cap) * (RR * 8 + 4);
+  const int in_smem = !L.shape.gate_global;
+  const size_t smem = in_smem ? static_cast<size_t>(A.nb_cap) * (RR * 8 + 4) : 0;
   cudaError_t e = allow_smem(paged_gate_kernel<D, RR>, static_cast<int>(smem), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -1105,7 +1411,7 @@ cudaError_t gate(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const int kt = kTileBytes / (D * (L.cache.fp8 ? 1 : 2));
+  const int kt = tile_bytes(L.cache.fp8) / (D * (L.cache.fp8 ? 1 : 2));
   return cudaLaunchKernelEx(&cfg, paged_gate_kernel<D, RR>, A, L.shape.rows_per_tile, kt, in_smem);
 }
 
@@ -1113,7 +1419,8 @@ template <int D>
 cudaError_t merge(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(A.nseq) * A.rows * A.Hq);
-  cfg.blockDim = dim3(128);
+  // a segment has about ctas * warps / nseg + 1 partials
+  cfg.blockDim = dim3(32 * (A.nseg >= 512 ? 2 : A.nseg >= 128 ? 4 : kMergeWarps));
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1131,19 +1438,23 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
   S.rows_per_tile = R <= 8 ? 8 : 16;
   S.nrt = (R + S.rows_per_tile - 1) / S.rows_per_tile;
   S.nseg = static_cast<long long>(P.nseq) * P.G * S.nrt;
-  const int kt = kTileBytes / (P.d * (P.fp8 ? 1 : 2));
+  const int kt = tile_bytes(P.fp8) / (P.d * (P.fp8 ? 1 : 2));
+  const int warps = paged_warps(P.fp8);
   const long long cap = static_cast<long long>(P.max_pages) << P.page_log;
   const long long tiles = S.nseg * ((cap + kt - 1) / kt);
-  S.ctas = static_cast<int>(std::min<long long>(sms, (tiles + kPagedWarps - 1) / kPagedWarps));
-  S.slots = static_cast<long long>(S.ctas) * kPagedWarps + S.nseg;
+  S.ctas = static_cast<int>(std::min<long long>(sms, (tiles + warps - 1) / warps));
+  S.slots = static_cast<long long>(S.ctas) * warps + S.nseg;
   if (topk) {
     S.nb_cap = static_cast<int>((cap + P.B - 1) / P.B);
     S.ent_cap = static_cast<int>(std::min<long long>(
         S.nb_cap, static_cast<long long>(std::min(R, S.rows_per_tile)) * topk));
     S.gate_ctas = 1;
-    while (S.gate_ctas < 8 && S.nb_cap > 128 * S.gate_ctas) S.gate_ctas *= 2;
+    // A CTA scores 32 blocks at a time. More CTAs per segment while they all run at once (two fit
+    // an SM); keys and marks of a single CTA stay in its shared memory where they fit.
+    while (S.gate_ctas < 8 && S.nb_cap > 64 * S.gate_ctas &&
+           S.nseg * S.gate_ctas * 2 <= 2 * kNumSms)
+      S.gate_ctas *= 2;
     const int rr = std::min(R, S.rows_per_tile);
-    // keys and marks of a small cache stay in shared memory
     S.gate_global = S.gate_ctas > 1 || static_cast<long long>(S.nb_cap) * (rr * 16 + 4) > 65536;
   }
   return S;

@@ -24,21 +24,32 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kIter = 4;  // rows per lane group in flight
 
+// Rotation of the lane's eight elements with weights folded in. An element pairs with its partner
+// o: y = x cx + o co in units of the normed row. Forward: cx = w c, co = w_o (-+ s), w_o the
+// partner's weight; without weights (backward): cx = c, co = -+ s.
 struct Rope {
-  float c[8], s[8];  // of the lane's eight elements; s carries the sign of the element's half
+  float cx[8], co[8];
 };
 
-// Table row of position p for the lane that holds elements 8l .. 8l+7. Elements at or behind
-// `rot` keep c = 1, s = 0. Half-split: element e < rot/2 pairs with e + rot/2, both read entry
-// e mod rot/2; rot is a multiple of 16, so a lane's elements lie in one half. Adjacent: (2i, 2i+1).
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p + 4));
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+// Table row of one position for the lane that holds elements 8l .. 8l+7. Elements at or behind
+// `rot` are not turned. Half-split: element e < rot/2 pairs with e + rot/2, both read entry
+// e mod rot/2; rot is a multiple of 16, so a lane's elements lie in one half and their partners in
+// lane l +- rot/16. Adjacent: (2i, 2i+1), in the lane itself. dir = -1 turns back.
 template <bool ADJ>
 __device__ __forceinline__ Rope load_rope(const float* __restrict__ row, int l, int rot,
                                           float dir) {
   Rope R;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    R.c[e] = 1.f;
-    R.s[e] = 0.f;
+    R.cx[e] = 1.f;
+    R.co[e] = 0.f;
   }
   if (8 * l < rot) {
     const int half = rot >> 1;
@@ -48,36 +59,37 @@ __device__ __forceinline__ Rope load_rope(const float* __restrict__ row, int l, 
       const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        R.c[e] = cv[e >> 1];
-        R.s[e] = (e & 1) ? dir * sv[e >> 1] : -dir * sv[e >> 1];
+        R.cx[e] = cv[e >> 1];
+        R.co[e] = (e & 1) ? dir * sv[e >> 1] : -dir * sv[e >> 1];
       }
     } else {
       const bool second = 8 * l >= half;
       const int at = 8 * l - (second ? half : 0);
       const float sign = second ? dir : -dir;
+      load8(row + at, R.cx);
+      load8(row + half + at, R.co);
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(row + at + e));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + at + e));
-        R.c[e] = c.x; R.c[e + 1] = c.y; R.c[e + 2] = c.z; R.c[e + 3] = c.w;
-        R.s[e] = sign * s.x; R.s[e + 1] = sign * s.y;
-        R.s[e + 2] = sign * s.z; R.s[e + 3] = sign * s.w;
-      }
+      for (int e = 0; e < 8; ++e) R.co[e] *= sign;
     }
   }
   return R;
 }
 
-// z <- z turned. Every lane of the warp must call it (shuffles); `partner` is the lane that holds
-// the other halves of the pairs (half-split form).
+// Lane that holds the partners of this lane's elements (half-split form; itself otherwise).
 template <bool ADJ>
-__device__ __forceinline__ void turn(float (&z)[8], const Rope& R, int partner) {
-  float o[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    o[e] = ADJ ? z[e ^ 1] : __shfl_sync(0xffffffffu, z[e], partner);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) z[e] = fmaf(z[e], R.c[e], o[e] * R.s[e]);
+__device__ __forceinline__ int partner_of(int l, int rot) {
+  const int hl = rot >> 4;  // lanes of one half
+  return ADJ || 8 * l >= rot ? l : l < hl ? l + hl : l - hl;
+}
+
+// The partner's eight elements: four packed pairs, exchanged between lanes or within them.
+template <bool ADJ>
+__device__ __forceinline__ uint4 swap_pairs(const uint4& u, int lane) {
+  if (ADJ)
+    return make_uint4(__byte_perm(u.x, 0, 0x1032), __byte_perm(u.y, 0, 0x1032),
+                      __byte_perm(u.z, 0, 0x1032), __byte_perm(u.w, 0, 0x1032));
+  return make_uint4(__shfl_sync(0xffffffffu, u.x, lane), __shfl_sync(0xffffffffu, u.y, lane),
+                    __shfl_sync(0xffffffffu, u.z, lane), __shfl_sync(0xffffffffu, u.w, lane));
 }
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
@@ -123,15 +135,17 @@ struct ChunkRows {
   static constexpr int kRows = kIter * (32 / (D / 8));
 };
 
+// y = r (x (w c) + x_o (w_o s)): the partner's bf16 pairs are exchanged as they were loaded, and
+// the weights go into the token's rotation once for all of the warp's rows.
 template <int D, bool ADJ>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormArgs A) {
+__global__ void __launch_bounds__(kNormThreads, 5) qk_norm_rope_kernel(const NormArgs A) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const long long unit =
-      (static_cast<long long>(blockIdx.x) * kNormThreads + threadIdx.x) >> 5;
+  const unsigned unit = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const long long t = unit / A.chunks;
-  if (t >= A.T) return;  // uniform over the warp
-  int chunk = static_cast<int>(unit - t * A.chunks);
+  const unsigned tok = unit / static_cast<unsigned>(A.chunks);
+  if (tok >= static_cast<unsigned>(A.T)) return;  // uniform over the warp
+  const long long t = tok;
+  int chunk = static_cast<int>(unit - tok * A.chunks);
   const bool isq = chunk < A.qchunks;
   if (!isq) chunk -= A.qchunks;
   const int H = isq ? A.Hq : A.Hkv, h0 = chunk * kIter * RPW + sub;
@@ -146,21 +160,24 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
   }
   const int p = __ldg(A.pos + t);
   const bool known = p >= 0 && p < A.n_pos;
-  const Rope R =
-      load_rope<ADJ>(A.rope + static_cast<size_t>(known ? p : 0) * A.rot, l, A.rot, 1.f);
-  const int hl = A.rot >> 4;  // lanes of one half
-  const int partner = lane + (8 * l >= A.rot ? 0 : l < hl ? hl : -hl);
-  const float* wp = (isq ? A.wq : A.wk) + l * 8;
-  float w[8];
+  Rope R = load_rope<ADJ>(A.rope + static_cast<size_t>(known ? p : 0) * A.rot, l, A.rot, 1.f);
+  const int pl = partner_of<ADJ>(l, A.rot), partner = lane - l + pl;
+  const float* wp = isq ? A.wq : A.wk;
+  {
+    float w[8], wo[8];
+    load8(wp + l * 8, w);
+    load8(wp + pl * 8, wo);
 #pragma unroll
-  for (int e = 0; e < 8; e += 4) {
-    const float4 f = __ldg(reinterpret_cast<const float4*>(wp + e));
-    w[e] = f.x; w[e + 1] = f.y; w[e + 2] = f.z; w[e + 3] = f.w;
+    for (int e = 0; e < 8; ++e) {
+      R.cx[e] *= w[e];
+      R.co[e] *= ADJ ? w[e ^ 1] : wo[e];
+    }
   }
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    float x[8];
+    float x[8], o[8];
     unpack8(raw[i], x);
+    unpack8(swap_pairs<ADJ>(raw[i], partner), o);
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
@@ -168,8 +185,7 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormAr
     // a position outside the table has no angle: the row becomes NaN instead of a wrong number
     const float r = known ? rsqrtf(ss * (1.f / D) + A.eps) : __int_as_float(0x7fffffff);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
-    turn<ADJ>(x, R, partner);
+    for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], R.cx[e], o[e] * R.co[e]) * r;
     const int h = h0 + i * RPW;
     if (h < H) __stcs(reinterpret_cast<uint4*>(dst + static_cast<size_t>(h) * D), pack8(x));
   }
@@ -192,15 +208,9 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_bwd_kernel(const No
   if (!isq) chunk -= A.qchunks;
   const int H = isq ? A.Hq : A.Hkv, h0 = chunk * kIter * RPW + sub;
   if (g < G) {
-    const int hl = A.rot >> 4;
-    const int partner = lane + (8 * l >= A.rot ? 0 : l < hl ? hl : -hl);
-    const float* wp = (isq ? A.wq : A.wk) + l * 8;
+    const int partner = lane - l + partner_of<ADJ>(l, A.rot);
     float w[8];
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(wp + e));
-      w[e] = f.x; w[e + 1] = f.y; w[e + 2] = f.z; w[e + 3] = f.w;
-    }
+    load8((isq ? A.wq : A.wk) + l * 8, w);
     for (long long t = g / A.chunks; t < A.T; t += G / A.chunks) {
       const __nv_bfloat16* xs = (isq ? A.q + t * A.q_ld : A.k + t * A.k_ld) + l * 8;
       const __nv_bfloat16* ys = (isq ? A.dyq : A.dyk) + t * H * D + l * 8;
@@ -220,10 +230,12 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_bwd_kernel(const No
           load_rope<ADJ>(A.rope + static_cast<size_t>(known ? p : 0) * A.rot, l, A.rot, -1.f);
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
-        float x[8], z[8];
+        float x[8], z[8], o[8];
         unpack8(xr[i], x);
         unpack8(yr[i], z);
-        turn<ADJ>(z, R, partner);
+        unpack8(swap_pairs<ADJ>(yr[i], partner), o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = fmaf(z[e], R.cx[e], o[e] * R.co[e]);
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
@@ -266,20 +278,22 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_bwd_kernel(const No
   }
 }
 
-// dw[x] = sum of the CTAs' parts, in CTA order within eight interleaved fp64 sums.
-__global__ void __launch_bounds__(256) qk_norm_dw_kernel(const float* __restrict__ part, int n,
-                                                         int D, float* __restrict__ dwq,
-                                                         float* __restrict__ dwk) {
-  __shared__ double red[8][33];
+// dw[x] = sum of the CTAs' parts: 32 interleaved fp64 sums, joined in order. One launch of a few
+// CTAs, so each thread has all its loads in flight at once.
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* __restrict__ part, int n,
+                                                          int D, float* __restrict__ dwq,
+                                                          float* __restrict__ dwk) {
+  __shared__ double red[32][33];
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5, x = blockIdx.x * 32 + c;
   double s = 0.;
-#pragma unroll 4
-  for (int i = w; i < n; i += 8) s += static_cast<double>(part[static_cast<size_t>(i) * 2 * D + x]);
+#pragma unroll 20
+  for (int i = w; i < n; i += 32)
+    s += static_cast<double>(part[static_cast<size_t>(i) * 2 * D + x]);
   red[w][c] = s;
   __syncthreads();
   if (w == 0) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][c];
+    for (int i = 1; i < 32; ++i) s += red[i][c];
     (x < D ? dwq[x] : dwk[x - D]) = static_cast<float>(s);
   }
 }
@@ -341,7 +355,7 @@ cudaError_t launch_qk_norm_bwd(const NormLaunch& L, int ctas, cudaStream_t s) {
 
 cudaError_t launch_qk_norm_dw(const float* part, int n, int d, float* dwq, float* dwk,
                               cudaStream_t s) {
-  qk_norm_dw_kernel<<<2 * d / 32, 256, 0, s>>>(part, n, d, dwq, dwk);
+  qk_norm_dw_kernel<<<2 * d / 32, 1024, 0, s>>>(part, n, d, dwq, dwk);
   return cudaGetLastError();
 }
 

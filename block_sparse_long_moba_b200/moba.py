@@ -491,20 +491,34 @@ def moba_attn_fwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     return o, lse
 
 
+def _is(t, dtype, shape, device) -> bool:
+    """The conditions of _want as one expression: the calls of a decode step take microseconds, so
+    they ask this first and _want says what is wrong."""
+    return (torch.is_tensor(t) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous())
+
+
+def _raw_stream(stream, device: torch.device) -> int:
+    """The cudaStream_t of `stream`, or of the device's current stream."""
+    return (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+            else stream.cuda_stream)
+
+
 def _rows(what: str, name: str, t: torch.Tensor, heads: Optional[int] = None,
           d: Optional[int] = None) -> int:
     """Checks bf16 [T, heads, d] whose heads are packed and whose tokens may lie further apart
     (a slice of a fused projection); returns the token stride in elements."""
     if not torch.is_tensor(t) or t.dim() != 3:
         _bad(what, f"{name} must be a 3-D tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         _bad(what, f"{name} must be {torch.bfloat16}, got {t.dtype}")
     T, h, w = t.shape
     if (heads is not None and h != heads) or (d is not None and w != d):
         _bad(what, f"{name} must have shape {(T, heads, d)}, got {tuple(t.shape)}")
-    if (w > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != w):
+    s0, s1, s2 = t.stride()
+    if (w > 1 and s2 != 1) or (h > 1 and s1 != w):
         _bad(what, f"{name}: the heads of a token must be packed, strides are {t.stride()}")
-    return t.stride(0) if T > 1 else h * w
+    return s0 if T > 1 else h * w
 
 
 def _workspace(nbytes: int, device, stream) -> torch.Tensor:
@@ -532,12 +546,16 @@ def _check_norm(what, q, k, q_weight, k_weight, rope, positions):
     k_ld = _rows(what, "k", k, d=d)
     if k.shape[0] != T or k.device != dev:
         _bad(what, f"k must have {T} tokens on {dev}, got {tuple(k.shape)} on {k.device}")
-    _want(what, "q_weight", q_weight, torch.float32, (d,), dev)
-    _want(what, "k_weight", k_weight, torch.float32, (d,), dev)
+    if not _is(q_weight, torch.float32, (d,), dev):
+        _want(what, "q_weight", q_weight, torch.float32, (d,), dev)
+    if not _is(k_weight, torch.float32, (d,), dev):
+        _want(what, "k_weight", k_weight, torch.float32, (d,), dev)
     if not torch.is_tensor(rope) or rope.dim() != 2:
         _bad(what, "rope must be a [n_pos, rot_dim] tensor")
-    _want(what, "rope", rope, torch.float32, None, dev)
-    _want(what, "positions", positions, torch.int32, (T,), dev)
+    if not _is(rope, torch.float32, rope.shape, dev):
+        _want(what, "rope", rope, torch.float32, None, dev)
+    if not _is(positions, torch.int32, (T,), dev):
+        _want(what, "positions", positions, torch.int32, (T,), dev)
     return dev, T, hq, k.shape[1], d, q_ld, k_ld
 
 
@@ -552,17 +570,17 @@ def moba_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
     what = "moba_qk_norm_rope"
     dev, T, hq, hkv, d, q_ld, k_ld = _check_norm(what, q, k, q_weight, k_weight, rope, positions)
     if q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
+        q_out = q.new_empty((T, hq, d))
     else:
         _want(what, "q_out", q_out, torch.bfloat16, (T, hq, d), dev)
     if k_out is None:
-        k_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=dev)
+        k_out = k.new_empty((T, hkv, d))
     else:
         _want(what, "k_out", k_out, torch.bfloat16, (T, hkv, d), dev)
     st = load_library().moba_qk_norm_rope(
         q.data_ptr(), q_ld, k.data_ptr(), k_ld, q_weight.data_ptr(), k_weight.data_ptr(),
         rope.data_ptr(), rope.shape[0], rope.shape[1], positions.data_ptr(), T, hq, hkv, d, eps,
-        1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), _stream(stream))
+        1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), _raw_stream(stream, dev))
     _check(st, what)
     return q_out, k_out
 
@@ -599,7 +617,7 @@ def moba_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tens
         rope.data_ptr(), rope.shape[0], rope.shape[1], positions.data_ptr(), d_q_out.data_ptr(),
         d_k_out.data_ptr(), T, hq, hkv, d, eps, 1 if interleaved else 0, dq.data_ptr(),
         dk.data_ptr(), d_q_weight.data_ptr(), d_k_weight.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _stream(stream))
+        workspace.numel(), _raw_stream(stream, dev))
     _check(st, what)
     return dq, dk, d_q_weight, d_k_weight
 
@@ -694,10 +712,11 @@ def moba_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor,
         _bad(what, f"k and v must have the same rows, got {k.shape[0]} and {v.shape[0]}")
     if k.device != dev or v.device != dev:
         _bad(what, f"k is on {k.device} and v on {v.device}, the cache on {dev}")
-    _want(what, "cu_seqlens_q", cu_seqlens_q, torch.int32, (cache.nseq + 1,), dev)
+    if not _is(cu_seqlens_q, torch.int32, (cache.nseq + 1,), dev):
+        _want(what, "cu_seqlens_q", cu_seqlens_q, torch.int32, (cache.nseq + 1,), dev)
     _check(load_library().moba_cache_append(cache._ref, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
                                             cu_seqlens_q.data_ptr(), k.shape[0],
-                                            _stream(stream)), what)
+                                            _raw_stream(stream, dev)), what)
 
 
 def moba_cache_read(cache: PagedCache, cu_seqlens: torch.Tensor, cu_seqlens_host,
@@ -718,7 +737,7 @@ def moba_cache_read(cache: PagedCache, cu_seqlens: torch.Tensor, cu_seqlens_host
     _want(what, "k", k, torch.bfloat16, shape, dev)
     _want(what, "v", v, torch.bfloat16, shape, dev)
     _check(load_library().moba_cache_read(cache._ref, cu_seqlens.data_ptr(), shape[0],
-                                          k.data_ptr(), v.data_ptr(), _stream(stream)), what)
+                                          k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev)), what)
     return k, v
 
 
@@ -731,7 +750,8 @@ def _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace, stream):
     if rows_per_seq < 1 or n != cache.nseq * rows_per_seq or d != cache.d:
         _bad(what, f"q must have shape {(cache.nseq * rows_per_seq, hq, cache.d)}, "
                    f"got {tuple(q.shape)}")
-    _want(what, "q", q, torch.bfloat16, None, dev)
+    if not _is(q, torch.bfloat16, q.shape, dev):
+        _want(what, "q", q, torch.bfloat16, None, dev)
     if o is None:
         o = torch.empty_like(q)
     else:
@@ -757,7 +777,7 @@ def moba_paged_attn_fwd(cache: PagedCache, q: torch.Tensor, rows_per_seq: int = 
     dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, 0, o, lse, workspace, stream)
     st = load_library().moba_paged_attn_fwd(
         cache._ref, q.data_ptr(), hq, rows_per_seq, cache.d ** -0.5 if scale is None else scale,
-        o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+        o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     _check(st, what)
     return o, lse
 
@@ -774,13 +794,13 @@ def moba_paged_decode_fwd(cache: PagedCache, q: torch.Tensor, topk: int, rows_pe
     if topk < 1 or not _cache(what, cache).block_size:
         _bad(what, "topk must be positive and the cache have block_sums")
     dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace, stream)
-    if block_idx_out is not None:
+    if block_idx_out is not None and not _is(block_idx_out, torch.int32, (hq, n, topk), dev):
         _want(what, "block_idx_out", block_idx_out, torch.int32, (hq, n, topk), dev)
     st = load_library().moba_paged_decode_fwd(
         cache._ref, q.data_ptr(), hq, rows_per_seq, topk,
         cache.d ** -0.5 if scale is None else scale,
         None if block_idx_out is None else block_idx_out.data_ptr(), o.data_ptr(), lse.data_ptr(),
-        ws.data_ptr(), ws.numel(), _stream(stream))
+        ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     _check(st, what)
     return o, lse
 

@@ -240,7 +240,7 @@ int moba_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long
  *              the device: they may change between calls, and between replays of a graph.
  *   page_size  a power of two, 16 .. 4096; block_size (read with block_sums only): a multiple of
  *              64 and of page_size. max_pages * page_size <= 2^30, Hkv <= 1024.
- * Entries of page_table behind a sequence's last page are not read. A page number outside
+ * Entries of page_table behind a sequence's last page are not used. A page number outside
  * [0, num_pages), or a seq_lens beyond max_pages * page_size, is never dereferenced: the calls
  * below say what becomes of it. Two sequences may share pages that no call writes.
  */
