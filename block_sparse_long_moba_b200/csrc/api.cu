@@ -827,7 +827,7 @@ int moba_qk_norm_rope(const void* q, long long q_stride, const void* k, long lon
 
 size_t moba_qk_norm_rope_bwd_workspace_bytes(int Hq, int Hkv, int d) {
   if (Hq < 1 || Hkv < 1 || Hq > 65536 || Hkv > 65536 || (d != 64 && d != 128)) return 0;
-  return up256(static_cast<size_t>(qk_norm_bwd_ctas(Hq, Hkv, d, kNumSms)) * 2 * d * 4);
+  return up256(static_cast<size_t>(qk_norm_bwd_ctas(Hq, Hkv, d, 0x7fffffff)) * 2 * d * 4);
 }
 
 int moba_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long long k_stride,
@@ -855,7 +855,7 @@ int moba_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long
   N.part = static_cast<float*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // no rows: the weights' gradients are zero (a sum over no CTA)
-  const int ctas = T > 0 ? qk_norm_bwd_ctas(Hq, Hkv, d, kNumSms) : 0;
+  const int ctas = T > 0 ? qk_norm_bwd_ctas(Hq, Hkv, d, T) : 0;
   if (T > 0)
     MOBA_LAUNCH_NAMED(-1, "moba_qk_norm_rope_bwd", s, launch_qk_norm_bwd(N, ctas, s));
   MOBA_LAUNCH_NAMED(-1, "moba_qk_norm_dw", s,

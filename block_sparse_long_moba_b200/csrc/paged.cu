@@ -29,6 +29,7 @@
 // Rounding: weights to bf16 (e4m3 cache: f16) for the second product; logits, maxima, sums (of the
 // unrounded weights) and outputs are fp32 until the final bf16.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
@@ -902,6 +903,7 @@ constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
 constexpr int kGateInRegs = 8;  // keys a thread holds in a selection
 constexpr int kGateWords = kMaxBlocksPerSeq / 32;
+constexpr int kGateSmem = 65536;  // for keys and marks
 
 __device__ __forceinline__ unsigned long long order_key64(double x) {
   if (x != x) return 0ull;  // NaN: behind every number
@@ -1364,19 +1366,20 @@ PagedArgs args_of(const PagedLaunch& L) {
 // Launch attributes are set once per device and kernel (a driver call that a decode step of a few
 // microseconds would notice).
 template <class K>
-cudaError_t allow_smem(K kernel, int bytes, int (&done)[64]) {
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<int> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev] >= bytes) return cudaSuccess;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed) >= bytes)
+    return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = bytes;
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(bytes, std::memory_order_relaxed);
   return e;
 }
 
 template <int D, bool FP8, int NT, bool SPARSE>
 cudaError_t attn(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
-  static int done[64];
+  static std::atomic<int> done[64];
   constexpr int smem = Tile<D, FP8>::kWarps * Tile<D, FP8>::kWarpBytes;
   cudaError_t e = allow_smem(paged_attn_kernel<D, FP8, NT, SPARSE>, smem, done);
   if (e != cudaSuccess) return e;
@@ -1395,10 +1398,10 @@ cudaError_t attn(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
 
 template <int D, int RR>
 cudaError_t gate(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
-  static int done[64];
+  static std::atomic<int> done[64];
   const int in_smem = !L.shape.gate_global;
   const size_t smem = in_smem ? static_cast<size_t>(A.nb_cap) * (RR * 8 + 4) : 0;
-  cudaError_t e = allow_smem(paged_gate_kernel<D, RR>, static_cast<int>(smem), done);
+  cudaError_t e = allow_smem(paged_gate_kernel<D, RR>, kGateSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(A.nseg) * L.shape.gate_ctas);
@@ -1455,7 +1458,7 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
            S.nseg * S.gate_ctas * 2 <= 2 * kNumSms)
       S.gate_ctas *= 2;
     const int rr = std::min(R, S.rows_per_tile);
-    S.gate_global = S.gate_ctas > 1 || static_cast<long long>(S.nb_cap) * (rr * 16 + 4) > 65536;
+    S.gate_global = S.gate_ctas > 1 || static_cast<long long>(S.nb_cap) * (rr * 16 + 4) > kGateSmem;
   }
   return S;
 }

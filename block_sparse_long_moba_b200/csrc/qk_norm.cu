@@ -7,115 +7,190 @@
 // All arithmetic is fp32 with one rounding to bf16 at the end; dw is summed per lane in fp32 over
 // its rows and across CTAs in fp64, in a fixed order.
 //
-// Bound: HBM. A row is read once and written once (backward: two reads, one write); 8-10 flops an
-// element are far below the FMA rate. D / 8 lanes hold one row in 16-byte pieces, so a pair of
-// the half-split rotation sits in two lanes (one shuffle per element) and the sum of squares is a
-// 3- or 4-step butterfly. A warp takes kIter rows of each lane group of one token, all loads
-// issued before the first use, and reads the token's table row once for all of them.
-#include <cmath>
+// Bound: HBM; a row is read once and written once (backward: two reads, one write). The arithmetic
+// is only ~10 flops an element, but at 23 bytes per clock and SM the instructions around it count:
+// the lanes of a row (d / 8 of them) hold both elements of each of their pairs, so a rotation needs
+// no exchange; products go two to an instruction; the sums of squares of a chunk's rows are reduced
+// together. Persistent: every warp takes a chunk of 2 KB (8 or 16 heads of one token) at a time
+// through a private ring in shared memory (16-byte cp.async, with the token's table row).
+#include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "launch.h"
+#include "sm100.cuh"
 
 namespace moba {
 
 namespace {
 
-constexpr int kNormThreads = 256;
-constexpr int kIter = 4;  // rows per lane group in flight
+constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
+constexpr int kIter = 4;  // 16-byte pieces of a chunk per lane
+constexpr int kChunkBytes = kIter * 512, kRopeBytes = 512;
 
-// Rotation of the lane's eight elements with weights folded in. An element pairs with its partner
-// o: y = x cx + o co in units of the normed row. Forward: cx = w c, co = w_o (-+ s), w_o the
-// partner's weight; without weights (backward): cx = c, co = -+ s.
-struct Rope {
-  float cx[8], co[8];
-};
+__host__ __device__ constexpr int stage_bytes(bool bwd) {
+  return (bwd ? 2 : 1) * kChunkBytes + kRopeBytes;
+}
+constexpr int norm_stages(bool bwd) { return bwd ? 3 : 5; }
+constexpr int norm_smem(bool bwd) { return kNormWarps * norm_stages(bwd) * stage_bytes(bwd); }
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p + 4));
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0 bytes read: the destination is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
 }
 
-// Table row of one position for the lane that holds elements 8l .. 8l+7. Elements at or behind
-// `rot` are not turned. Half-split: element e < rot/2 pairs with e + rot/2, both read entry
-// e mod rot/2; rot is a multiple of 16, so a lane's elements lie in one half and their partners in
-// lane l +- rot/16. Adjacent: (2i, 2i+1), in the lane itself. dir = -1 turns back.
+// Multiplies and adds two to an instruction (f32x2).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// A lane's eight elements of a row: the first and the second elements of its four pairs.
+struct Elems {
+  float2 a[2], b[2];
+};
+
+// Where they lie. Lane l < rot/8 has pairs 4l .. 4l+3, the other lanes the elements behind rot.
+// Half-split: elements A .. A+3 and B .. B+3. Adjacent: elements A .. A+7, pairs neighbours.
 template <bool ADJ>
-__device__ __forceinline__ Rope load_rope(const float* __restrict__ row, int l, int rot,
-                                          float dir) {
-  Rope R;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    R.cx[e] = 1.f;
-    R.co[e] = 0.f;
+struct Place {
+  int A, B;
+  __device__ __forceinline__ Place(int l, int rot) {
+    const bool turned = 8 * l < rot;
+    A = ADJ || !turned ? 8 * l : 4 * l;
+    B = ADJ || !turned ? 8 * l + 4 : (rot >> 1) + 4 * l;
   }
-  if (8 * l < rot) {
-    const int half = rot >> 1;
-    if (ADJ) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + 4 * l));
-      const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+  __device__ __forceinline__ int col(bool second, int i) const {  // of element i of a or b
+    return ADJ ? A + 2 * i + second : (second ? B : A) + i;
+  }
+};
+
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <bool ADJ>
+__device__ __forceinline__ Elems read_row(const uint8_t* row, const Place<ADJ>& P) {
+  Elems x;
+  if (ADJ) {
+    const uint4 u = *reinterpret_cast<const uint4*>(row + 2 * P.A);
+    x.a[0] = make_float2(lo_f(u.x), lo_f(u.y));
+    x.a[1] = make_float2(lo_f(u.z), lo_f(u.w));
+    x.b[0] = make_float2(hi_f(u.x), hi_f(u.y));
+    x.b[1] = make_float2(hi_f(u.z), hi_f(u.w));
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(row + 2 * P.A);
+    const uint2 v = *reinterpret_cast<const uint2*>(row + 2 * P.B);
+    x.a[0] = make_float2(lo_f(u.x), hi_f(u.x));
+    x.a[1] = make_float2(lo_f(u.y), hi_f(u.y));
+    x.b[0] = make_float2(lo_f(v.x), hi_f(v.x));
+    x.b[1] = make_float2(lo_f(v.y), hi_f(v.y));
+  }
+  return x;
+}
+
+template <bool ADJ>
+__device__ __forceinline__ void write_row(__nv_bfloat16* row, const Place<ADJ>& P,
+                                          const Elems& x) {
+  if (ADJ) {
+    __stcs(reinterpret_cast<uint4*>(row + P.A),
+           make_uint4(pack2(x.a[0].x, x.b[0].x), pack2(x.a[0].y, x.b[0].y),
+                      pack2(x.a[1].x, x.b[1].x), pack2(x.a[1].y, x.b[1].y)));
+  } else {
+    __stcs(reinterpret_cast<uint2*>(row + P.A),
+           make_uint2(pack2(x.a[0].x, x.a[0].y), pack2(x.a[1].x, x.a[1].y)));
+    __stcs(reinterpret_cast<uint2*>(row + P.B),
+           make_uint2(pack2(x.b[0].x, x.b[0].y), pack2(x.b[1].x, x.b[1].y)));
+  }
+}
+
+template <bool ADJ>
+__device__ __forceinline__ Elems read_weights(const float* w, const Place<ADJ>& P) {
+  Elems x;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        R.cx[e] = cv[e >> 1];
-        R.co[e] = (e & 1) ? dir * sv[e >> 1] : -dir * sv[e >> 1];
-      }
-    } else {
-      const bool second = 8 * l >= half;
-      const int at = 8 * l - (second ? half : 0);
-      const float sign = second ? dir : -dir;
-      load8(row + at, R.cx);
-      load8(row + half + at, R.co);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) R.co[e] *= sign;
-    }
+  for (int i = 0; i < 2; ++i) {
+    x.a[i] = make_float2(w[P.col(false, 2 * i)], w[P.col(false, 2 * i + 1)]);
+    x.b[i] = make_float2(w[P.col(true, 2 * i)], w[P.col(true, 2 * i + 1)]);
+  }
+  return x;
+}
+
+// Cosines and sines of the lane's four pairs; 1 and 0 behind rot.
+struct Angle {
+  float2 c[2], s[2];
+};
+__device__ __forceinline__ Angle read_angle(const float* row, int l, int rot, bool all) {
+  Angle R;
+  const int at = all || 8 * l < rot ? 4 * l : 0;
+  const float4 c = *reinterpret_cast<const float4*>(row + at);
+  const float4 s = *reinterpret_cast<const float4*>(row + (rot >> 1) + at);
+  R.c[0] = make_float2(c.x, c.y);
+  R.c[1] = make_float2(c.z, c.w);
+  R.s[0] = make_float2(s.x, s.y);
+  R.s[1] = make_float2(s.z, s.w);
+  if (!all && 8 * l >= rot) {
+    R.c[0] = R.c[1] = make_float2(1.f, 1.f);
+    R.s[0] = R.s[1] = make_float2(0.f, 0.f);
   }
   return R;
 }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
 
-// Lane that holds the partners of this lane's elements (half-split form; itself otherwise).
-template <bool ADJ>
-__device__ __forceinline__ int partner_of(int l, int rot) {
-  const int hl = rot >> 4;  // lanes of one half
-  return ADJ || 8 * l >= rot ? l : l < hl ? l + hl : l - hl;
-}
-
-// The partner's eight elements: four packed pairs, exchanged between lanes or within them.
-template <bool ADJ>
-__device__ __forceinline__ uint4 swap_pairs(const uint4& u, int lane) {
-  if (ADJ)
-    return make_uint4(__byte_perm(u.x, 0, 0x1032), __byte_perm(u.y, 0, 0x1032),
-                      __byte_perm(u.z, 0, 0x1032), __byte_perm(u.w, 0, 0x1032));
-  return make_uint4(__shfl_sync(0xffffffffu, u.x, lane), __shfl_sync(0xffffffffu, u.y, lane),
-                    __shfl_sync(0xffffffffu, u.z, lane), __shfl_sync(0xffffffffu, u.w, lane));
-}
-
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Sums of N values over the LPR lanes of a row, all at once: on the way down a lane keeps half of
+// its values and hands over the other half, so that after log2 N steps it holds one value and the
+// shuffles are N - 1 + log2(LPR / N) instead of N log2 LPR. Lane l ends with the sum of value
+// l / (LPR / N).
+template <int LPR, int N>
+__device__ __forceinline__ float reduce_rows(float (&v)[N], int l) {
+  int n = N;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = __uint_as_float(w[e] << 16);
-    x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+  for (int o = LPR / 2; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        if (i < n) {
+          const float give = (l & o) ? v[i] : v[i + n], keep = (l & o) ? v[i + n] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
   }
+  return v[0];
 }
-
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint32_t w[4];
+// The way back: every lane of the row gets all N values.
+template <int LPR, int N>
+__device__ __forceinline__ void gather_rows(float mine, float (&v)[N], int l) {
+  v[0] = mine;
+  int n = 1;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-    w[e] = *reinterpret_cast<const uint32_t*>(&b);
+  for (int o = LPR / N; o < LPR; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      if (i < n) {
+        const float other = __shfl_xor_sync(0xffffffffu, v[i], o);
+        v[i + n] = (l & o) ? v[i] : other;
+        v[i] = (l & o) ? other : v[i];
+      }
+    n <<= 1;
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
 }
 
 struct NormArgs {
@@ -129,152 +204,181 @@ struct NormArgs {
   float eps;
 };
 
-// A chunk is kIter * (32 / LPR) consecutive heads of q, or of k.
-template <int D>
-struct ChunkRows {
-  static constexpr int kRows = kIter * (32 / (D / 8));
-};
+// A chunk is kIter * (32 / LPR) consecutive heads of q, or of k: 2 KB.
+__host__ __device__ constexpr int chunk_rows(int d) { return kChunkBytes / (2 * d); }
 
-// y = r (x (w c) + x_o (w_o s)): the partner's bf16 pairs are exchanged as they were loaded, and
-// the weights go into the token's rotation once for all of the warp's rows.
-template <int D, bool ADJ>
-__global__ void __launch_bounds__(kNormThreads, 5) qk_norm_rope_kernel(const NormArgs A) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const unsigned unit = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const unsigned tok = unit / static_cast<unsigned>(A.chunks);
-  if (tok >= static_cast<unsigned>(A.T)) return;  // uniform over the warp
-  const long long t = tok;
-  int chunk = static_cast<int>(unit - tok * A.chunks);
+// Warp g of G (G a multiple of the chunks per token) takes units g, g + G, ..., all of the same
+// chunk, so that its weights stay in registers and its dw sums belong to q or to k alone.
+// Forward: y_a = r (x_a (w_a c) - x_b (w_b s)), y_b = r (x_b (w_b c) + x_a (w_a s)), the weights
+// multiplied into the token's angle once for all rows of the chunk. Backward: as stated at the top.
+template <int D, bool ADJ, bool BWD>
+__global__ void __launch_bounds__(kNormThreads, 2) qk_norm_rope_kernel(const NormArgs A) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, kStage = stage_bytes(BWD);
+  constexpr int kStages = norm_stages(BWD);
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[BWD ? kNormWarps : 1][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
+  const int G = static_cast<int>(gridDim.x) * kNormWarps / A.chunks * A.chunks;
+  const int g = static_cast<int>(blockIdx.x) * kNormWarps + warp;
+  int chunk = g % A.chunks;
   const bool isq = chunk < A.qchunks;
   if (!isq) chunk -= A.qchunks;
-  const int H = isq ? A.Hq : A.Hkv, h0 = chunk * kIter * RPW + sub;
-  const __nv_bfloat16* src = (isq ? A.q + t * A.q_ld : A.k + t * A.k_ld) + l * 8;
-  __nv_bfloat16* dst = (isq ? A.oq : A.ok) + t * H * D + l * 8;
-  uint4 raw[kIter];
+  const int H = isq ? A.Hq : A.Hkv, h0 = chunk * chunk_rows(D) + sub;
+  const Place<ADJ> P(l, A.rot);
+  Elems acc;
 #pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const int h = h0 + i * RPW;
-    raw[i] = h < H ? __ldcs(reinterpret_cast<const uint4*>(src + static_cast<size_t>(h) * D))
-                   : make_uint4(0, 0, 0, 0);
+  for (int e = 0; e < 2; ++e) acc.a[e] = acc.b[e] = make_float2(0.f, 0.f);
+  const int step = G / A.chunks, t0 = g / A.chunks;  // tokens t0, t0 + step, ...
+  if (g < G && t0 < A.T) {
+    const long long x_step = (isq ? A.q_ld : A.k_ld) * step;
+    const long long y_step = static_cast<long long>(H) * D * step;
+    // where this lane's 16 bytes of the chunk's first rows come from, and its row goes to
+    const size_t at = static_cast<size_t>(h0) * D;
+    const __nv_bfloat16* xs = (isq ? A.q : A.k) + at + l * 8 + (isq ? A.q_ld : A.k_ld) * t0;
+    const __nv_bfloat16* ys =
+        BWD ? (isq ? A.dyq : A.dyk) + at + l * 8 + static_cast<size_t>(t0) * H * D : nullptr;
+    __nv_bfloat16* dst = (isq ? A.oq : A.ok) + at + static_cast<size_t>(t0) * H * D;
+    const Elems w = read_weights<ADJ>(isq ? A.wq : A.wk, P);
+    uint8_t* ring = smem + warp * (kStages * kStage);
+    const bool all = A.rot == D;
+    const int rot16 = A.rot >> 2;  // 16-byte pieces of a table row
+    bool in[kIter];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) in[i] = h0 + i * RPW < H;
+    // lane x fetches the position of the warp's unit n0 + x; 32 units at a time
+    auto positions = [&](int n0) {
+      const long long t = t0 + static_cast<long long>(n0 + lane) * step;
+      return t < A.T ? __ldg(A.pos + t) : -1;
+    };
+    const int units = (A.T - t0 + step - 1) / step;
+    int pos = positions(0);
+    const uint32_t lane_dst = smem_u32(ring) + lane * 16;
+    auto issue = [&](int n, int stage) {  // copies of the warp's unit n
+      if (n < units) {
+        const uint32_t d = lane_dst + stage * kStage;
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          copy16(d + i * 512, xs + (in[i] ? i * RPW * D : 0), in[i]);
+          if (BWD) copy16(d + kChunkBytes + i * 512, ys + (in[i] ? i * RPW * D : 0), in[i]);
+        }
+        const int p = __shfl_sync(0xffffffffu, pos, n & 31);
+        const bool known = p >= 0 && p < A.n_pos;
+        if (lane < rot16)
+          copy16(d + kStage - kRopeBytes,
+                 A.rope + static_cast<size_t>(known ? p : 0) * A.rot + lane * 4, true);
+        xs += x_step;
+        if (BWD) ys += y_step;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+    int was = pos;  // positions of the 32 units that the one in work belongs to
+    int stage = 0;
+    for (int n = 0; n < units; ++n) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();  // the unit is there; the stage of the last one is free
+      if ((n & 31) == 0) was = pos;
+      if (((n + kStages - 1) & 31) == 0) pos = positions(n + kStages - 1);
+      issue(n + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+      const int p = __shfl_sync(0xffffffffu, was, n & 31);
+      const bool known = p >= 0 && p < A.n_pos;
+      const uint8_t* s = ring + stage * kStage;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      const Angle R =
+          read_angle(reinterpret_cast<const float*>(s + kStage - kRopeBytes), l, A.rot, all);
+      Elems wc, ws;  // forward: weights times cosine, times sine (w_b's negative)
+      if (!BWD)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          wc.a[e] = mul2(w.a[e], R.c[e]);
+          wc.b[e] = mul2(w.b[e], R.c[e]);
+          ws.a[e] = mul2(w.a[e], R.s[e]);
+          ws.b[e] = mul2(neg2(w.b[e]), R.s[e]);
+        }
+      s += sub * 2 * D;
+      constexpr int NB = BWD ? 2 : kIter, N = 4;  // rows and sums of a batch (registers)
+#pragma unroll
+      for (int i0 = 0; i0 < kIter; i0 += NB) {
+        // the rows' sums first, all together, so that their shuffles overlap
+        Elems x[NB], z[BWD ? NB : 1];  // backward: z = dz
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          x[i] = read_row<ADJ>(s + (i0 + i) * 512, P);
+          float2 sq = mul2(x[i].a[0], x[i].a[0]);
+          sq = fma2(x[i].a[1], x[i].a[1], sq);
+          sq = fma2(x[i].b[0], x[i].b[0], sq);
+          sq = fma2(x[i].b[1], x[i].b[1], sq);
+          v[i] = sq.x + sq.y;
+          if constexpr (BWD) {
+            const Elems y = read_row<ADJ>(s + kChunkBytes + (i0 + i) * 512, P);
+            float2 dt = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              z[i].a[e] = fma2(y.a[e], R.c[e], mul2(y.b[e], R.s[e]));
+              z[i].b[e] = fma2(y.b[e], R.c[e], mul2(neg2(y.a[e]), R.s[e]));
+              dt = fma2(mul2(z[i].a[e], w.a[e]), x[i].a[e], dt);
+              dt = fma2(mul2(z[i].b[e], w.b[e]), x[i].b[e], dt);
+            }
+            v[NB + i] = dt.x + dt.y;  // times r: sum of dz w (x r)
+          }
+        }
+        float sum = reduce_rows<LPR, N>(v, l);
+        // the lanes that hold a sum of squares turn it into r; a position outside the table has
+        // no angle: the row becomes NaN, not a wrong number
+        if (!BWD || l < LPR / 2)
+          sum = known ? rsqrtf(sum * (1.f / D) + A.eps) : __int_as_float(0x7fffffff);
+        gather_rows<LPR, N>(sum, v, l);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const float2 r2 = make_float2(v[i], v[i]);
+          Elems y;
+          if constexpr (!BWD) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              y.a[e] = mul2(fma2(x[i].a[e], wc.a[e], mul2(x[i].b[e], ws.b[e])), r2);
+              y.b[e] = mul2(fma2(x[i].b[e], wc.b[e], mul2(x[i].a[e], ws.a[e])), r2);
+            }
+          } else {
+            const float dot = -v[NB + i] * v[i] * (1.f / D);
+            const float2 d2 = make_float2(dot, dot);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 xa = mul2(x[i].a[e], r2), xb = mul2(x[i].b[e], r2);
+              if (in[i0 + i]) {
+                acc.a[e] = fma2(z[i].a[e], xa, acc.a[e]);
+                acc.b[e] = fma2(z[i].b[e], xb, acc.b[e]);
+              }
+              y.a[e] = mul2(r2, fma2(xa, d2, mul2(z[i].a[e], w.a[e])));
+              y.b[e] = mul2(r2, fma2(xb, d2, mul2(z[i].b[e], w.b[e])));
+            }
+          }
+          if (in[i0 + i]) write_row<ADJ>(dst + (i0 + i) * RPW * D, P, y);
+        }
+      }
+      dst += y_step;
+    }
   }
-  const int p = __ldg(A.pos + t);
-  const bool known = p >= 0 && p < A.n_pos;
-  Rope R = load_rope<ADJ>(A.rope + static_cast<size_t>(known ? p : 0) * A.rot, l, A.rot, 1.f);
-  const int pl = partner_of<ADJ>(l, A.rot), partner = lane - l + pl;
-  const float* wp = isq ? A.wq : A.wk;
-  {
-    float w[8], wo[8];
-    load8(wp + l * 8, w);
-    load8(wp + pl * 8, wo);
+  if constexpr (BWD) {
+    // lanes of the same columns, then the CTA's warps of q and of k
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      R.cx[e] *= w[e];
-      R.co[e] *= ADJ ? w[e ^ 1] : wo[e];
+      const float2 pr = e < 4 ? acc.a[(e >> 1) & 1] : acc.b[(e >> 1) & 1];
+      float f = e & 1 ? pr.y : pr.x;
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+      if (sub == 0) red[warp][P.col(e >= 4, e & 3)] = f;
     }
-  }
-#pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    float x[8], o[8];
-    unpack8(raw[i], x);
-    unpack8(swap_pairs<ADJ>(raw[i], partner), o);
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-    ss = row_sum<LPR>(ss);
-    // a position outside the table has no angle: the row becomes NaN instead of a wrong number
-    const float r = known ? rsqrtf(ss * (1.f / D) + A.eps) : __int_as_float(0x7fffffff);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], R.cx[e], o[e] * R.co[e]) * r;
-    const int h = h0 + i * RPW;
-    if (h < H) __stcs(reinterpret_cast<uint4*>(dst + static_cast<size_t>(h) * D), pack8(x));
-  }
-}
-
-// Persistent: warp g of G (G a multiple of the chunks per token) takes units g, g + G, ..., all of
-// the same chunk, so its weights stay in registers and its dw sums belong to q or to k alone.
-template <int D, bool ADJ>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_rope_bwd_kernel(const NormArgs A) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, NW = kNormThreads / 32;
-  __shared__ float red[NW][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
-  const long long G = static_cast<long long>(gridDim.x) * NW / A.chunks * A.chunks;
-  const long long g = static_cast<long long>(blockIdx.x) * NW + warp;
-  float acc[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  int chunk = static_cast<int>(g % A.chunks);
-  const bool isq = chunk < A.qchunks;
-  if (!isq) chunk -= A.qchunks;
-  const int H = isq ? A.Hq : A.Hkv, h0 = chunk * kIter * RPW + sub;
-  if (g < G) {
-    const int partner = lane - l + partner_of<ADJ>(l, A.rot);
-    float w[8];
-    load8((isq ? A.wq : A.wk) + l * 8, w);
-    for (long long t = g / A.chunks; t < A.T; t += G / A.chunks) {
-      const __nv_bfloat16* xs = (isq ? A.q + t * A.q_ld : A.k + t * A.k_ld) + l * 8;
-      const __nv_bfloat16* ys = (isq ? A.dyq : A.dyk) + t * H * D + l * 8;
-      __nv_bfloat16* dst = (isq ? A.oq : A.ok) + t * H * D + l * 8;
-      uint4 xr[kIter], yr[kIter];
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int h = h0 + i * RPW;
-        const bool in = h < H;
-        const size_t at = static_cast<size_t>(h) * D;
-        xr[i] = in ? __ldcs(reinterpret_cast<const uint4*>(xs + at)) : make_uint4(0, 0, 0, 0);
-        yr[i] = in ? __ldcs(reinterpret_cast<const uint4*>(ys + at)) : make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int x = threadIdx.x; x < 2 * D; x += kNormThreads) {
+      float s = 0.f;
+      for (int i = 0; i < kNormWarps; ++i) {
+        const int gi = static_cast<int>(blockIdx.x) * kNormWarps + i;
+        if (gi < G && (gi % A.chunks < A.qchunks) == (x < D)) s += red[i][x % D];
       }
-      const int p = __ldg(A.pos + t);
-      const bool known = p >= 0 && p < A.n_pos;
-      const Rope R =
-          load_rope<ADJ>(A.rope + static_cast<size_t>(known ? p : 0) * A.rot, l, A.rot, -1.f);
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        float x[8], z[8], o[8];
-        unpack8(xr[i], x);
-        unpack8(yr[i], z);
-        unpack8(swap_pairs<ADJ>(yr[i], partner), o);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = fmaf(z[e], R.cx[e], o[e] * R.co[e]);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        ss = row_sum<LPR>(ss);
-        const float r = known ? rsqrtf(ss * (1.f / D) + A.eps) : __int_as_float(0x7fffffff);
-        float dot = 0.f;
-        const bool in = h0 + i * RPW < H;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] *= r;  // x r
-          if (in) acc[e] = fmaf(z[e], x[e], acc[e]);
-          z[e] *= w[e];
-          dot = fmaf(z[e], x[e], dot);
-        }
-        dot = row_sum<LPR>(dot) * (1.f / D);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = r * fmaf(-x[e], dot, z[e]);
-        if (in)
-          __stcs(reinterpret_cast<uint4*>(dst + static_cast<size_t>(h0 + i * RPW) * D), pack8(x));
-      }
+      A.part[static_cast<size_t>(blockIdx.x) * 2 * D + x] = s;
     }
-  }
-  // lanes of the same columns, then the CTA's warps of q and of k
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-#pragma unroll
-    for (int o = LPR; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
-    if (sub == 0) red[warp][l * 8 + e] = acc[e];
-  }
-  __syncthreads();
-  for (int x = threadIdx.x; x < 2 * D; x += kNormThreads) {
-    const int which = x / D;  // 0: q, 1: k
-    float s = 0.f;
-    for (int i = 0; i < NW; ++i) {
-      const long long gi = static_cast<long long>(blockIdx.x) * NW + i;
-      const int ci = static_cast<int>(gi % A.chunks);
-      if (gi < G && (ci < A.qchunks) == (which == 0)) s += red[i][x % D];
-    }
-    A.part[static_cast<size_t>(blockIdx.x) * 2 * D + x] = s;
   }
 }
 
@@ -310,47 +414,62 @@ NormArgs args_of(const NormLaunch& L) {
   A.ok = static_cast<__nv_bfloat16*>(L.ok);
   A.part = L.part;
   A.T = L.T; A.Hq = L.Hq; A.Hkv = L.Hkv; A.n_pos = L.n_pos; A.rot = L.rot;
-  const int rows = L.d == 64 ? ChunkRows<64>::kRows : ChunkRows<128>::kRows;
-  A.qchunks = (L.Hq + rows - 1) / rows;
-  A.chunks = A.qchunks + (L.Hkv + rows - 1) / rows;
+  A.qchunks = (L.Hq + chunk_rows(L.d) - 1) / chunk_rows(L.d);
+  A.chunks = A.qchunks + (L.Hkv + chunk_rows(L.d) - 1) / chunk_rows(L.d);
   A.eps = L.eps;
   return A;
 }
 
+// CTAs: what fits the SMs at once (two of 8 warps, their rings 100 or 108 KB), at least a warp
+// for every chunk of a token, and no more than there are units.
+int norm_ctas(int chunks, long long T) {
+  const long long all = (T * chunks + kNormWarps - 1) / kNormWarps;
+  const long long most = 2ll * kNumSms;
+  return static_cast<int>(std::max<long long>(std::min(all, most),
+                                              (chunks + kNormWarps - 1) / kNormWarps));
+}
+
+template <int D, bool ADJ, bool BWD>
+cudaError_t launch(const NormArgs& A, int ctas, cudaStream_t s) {
+  static std::atomic<int> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(qk_norm_rope_kernel<D, ADJ, BWD>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, norm_smem(BWD));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_relaxed);
+  }
+  qk_norm_rope_kernel<D, ADJ, BWD><<<ctas, kNormThreads, norm_smem(BWD), s>>>(A);
+  return cudaGetLastError();
+}
+
+template <bool BWD>
+cudaError_t launch_any(const NormLaunch& L, int ctas, cudaStream_t s) {
+  const NormArgs A = args_of(L);
+  if (L.d == 64)
+    return L.adjacent ? launch<64, true, BWD>(A, ctas, s) : launch<64, false, BWD>(A, ctas, s);
+  return L.adjacent ? launch<128, true, BWD>(A, ctas, s) : launch<128, false, BWD>(A, ctas, s);
+}
+
+int chunks_of(int Hq, int Hkv, int d) {
+  const int rows = chunk_rows(d);
+  return (Hq + rows - 1) / rows + (Hkv + rows - 1) / rows;
+}
+
 }  // namespace
 
-// CTAs of the backward kernel: four per SM, enough warps for every chunk of a token.
-int qk_norm_bwd_ctas(int Hq, int Hkv, int d, int sms) {
-  const int rows = d == 64 ? ChunkRows<64>::kRows : ChunkRows<128>::kRows;
-  const int chunks = (Hq + rows - 1) / rows + (Hkv + rows - 1) / rows;
-  const int nw = kNormThreads / 32;
-  return (4 * sms > (chunks + nw - 1) / nw) ? 4 * sms : (chunks + nw - 1) / nw;
+int qk_norm_bwd_ctas(int Hq, int Hkv, int d, int T) {
+  return norm_ctas(chunks_of(Hq, Hkv, d), T);
 }
 
 cudaError_t launch_qk_norm(const NormLaunch& L, cudaStream_t s) {
-  const NormArgs A = args_of(L);
-  const long long warps = static_cast<long long>(A.T) * A.chunks;
-  const unsigned grid = static_cast<unsigned>((warps + kNormThreads / 32 - 1) / (kNormThreads / 32));
-  if (L.d == 64) {
-    if (L.adjacent) qk_norm_rope_kernel<64, true><<<grid, kNormThreads, 0, s>>>(A);
-    else qk_norm_rope_kernel<64, false><<<grid, kNormThreads, 0, s>>>(A);
-  } else {
-    if (L.adjacent) qk_norm_rope_kernel<128, true><<<grid, kNormThreads, 0, s>>>(A);
-    else qk_norm_rope_kernel<128, false><<<grid, kNormThreads, 0, s>>>(A);
-  }
-  return cudaGetLastError();
+  return launch_any<false>(L, norm_ctas(chunks_of(L.Hq, L.Hkv, L.d), L.T), s);
 }
 
 cudaError_t launch_qk_norm_bwd(const NormLaunch& L, int ctas, cudaStream_t s) {
-  const NormArgs A = args_of(L);
-  if (L.d == 64) {
-    if (L.adjacent) qk_norm_rope_bwd_kernel<64, true><<<ctas, kNormThreads, 0, s>>>(A);
-    else qk_norm_rope_bwd_kernel<64, false><<<ctas, kNormThreads, 0, s>>>(A);
-  } else {
-    if (L.adjacent) qk_norm_rope_bwd_kernel<128, true><<<ctas, kNormThreads, 0, s>>>(A);
-    else qk_norm_rope_bwd_kernel<128, false><<<ctas, kNormThreads, 0, s>>>(A);
-  }
-  return cudaGetLastError();
+  return launch_any<true>(L, ctas, s);
 }
 
 cudaError_t launch_qk_norm_dw(const float* part, int n, int d, float* dwq, float* dwk,
