@@ -2,7 +2,10 @@
 
 Every step of the MoBA forward pass runs in the library's CUDA kernels; PyTorch only provides
 device memory and the current stream. The functions mirror the C entry points of include/moba.h
-and raise if the library is missing or a call fails — there is no fallback path.
+and raise if the library is missing or a call fails — there is no fallback path. The calls around
+the paged cache, which a decode step makes in microseconds, marshal their arguments in csrc/bind.cpp
+where these are plain (on the current stream, all as documented); the checks here handle the rest and
+say what is wrong.
 """
 from __future__ import annotations
 
@@ -43,17 +46,23 @@ class MobaError(RuntimeError):
 
 
 _lib = None
+_bind = None  # csrc/bind.cpp, once the library is loaded
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libmoba.so, or libmoba_checks.so when MOBA_CHECKS=1 (build them with
     `python -m block_sparse_long_moba_b200.build [--checks]`)."""
-    global _lib
+    global _lib, _bind
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
         raise ImportError(f"libmoba.so not found at {path}; build it with "
                           "`python -m block_sparse_long_moba_b200.build`")
+    try:
+        from . import _bind as bind
+    except ImportError as e:
+        raise ImportError(f"the binding's _bind.so is missing or does not load ({e}); build it "
+                          "with `python -m block_sparse_long_moba_b200.build`") from e
     lib = ctypes.CDLL(path)
     P, I, L, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
     lib.moba_status_string.argtypes = [I]
@@ -113,7 +122,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moba_paged_attn_fwd.restype = I
     lib.moba_paged_decode_fwd.argtypes = [P, P, I, I, I, F, P, P, P, P, S, P]
     lib.moba_paged_decode_fwd.restype = I
-    _lib = lib
+    bind.init(*(ctypes.cast(f, P).value for f in (
+        lib.moba_qk_norm_rope, lib.moba_qk_norm_rope_bwd,
+        lib.moba_qk_norm_rope_bwd_workspace_bytes, lib.moba_cache_append, lib.moba_cache_read,
+        lib.moba_paged_attn_fwd, lib.moba_paged_decode_fwd)))
+    _lib, _bind = lib, bind
     return lib
 
 
@@ -504,6 +517,13 @@ def _raw_stream(stream, device: torch.device) -> int:
             else stream.cuda_stream)
 
 
+def _done(result, what: str):
+    """What a call through csrc/bind.cpp returned: its outputs, or a status that is not MOBA_OK."""
+    if type(result) is int:
+        _check(result, what)
+    return result
+
+
 def _rows(what: str, name: str, t: torch.Tensor, heads: Optional[int] = None,
           d: Optional[int] = None) -> int:
     """Checks bf16 [T, heads, d] whose heads are packed and whose tokens may lie further apart
@@ -568,6 +588,11 @@ def moba_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
     weights [d], and the rotary position of positions [T] in a table from rope_table. Returns
     packed (q_out, k_out)."""
     what = "moba_qk_norm_rope"
+    if stream is None and _bind is not None:
+        done = _bind.norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved, q_out,
+                               k_out)
+        if done is not None:
+            return _done(done, what)
     dev, T, hq, hkv, d, q_ld, k_ld = _check_norm(what, q, k, q_weight, k_weight, rope, positions)
     if q_out is None:
         q_out = q.new_empty((T, hq, d))
@@ -596,6 +621,12 @@ def moba_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tens
     """Gradients (dq, dk, d_q_weight, d_k_weight) of moba_qk_norm_rope; nothing but its inputs is
     needed from the forward pass."""
     what = "moba_qk_norm_rope_bwd"
+    if (stream is None and _bind is not None and dq is None and dk is None and d_q_weight is None
+            and d_k_weight is None and workspace is None):
+        done = _bind.norm_rope_bwd(q, k, q_weight, k_weight, rope, positions, d_q_out, d_k_out,
+                                   eps, interleaved)
+        if done is not None:
+            return _done(done, what)
     dev, T, hq, hkv, d, q_ld, k_ld = _check_norm(what, q, k, q_weight, k_weight, rope, positions)
     _want(what, "d_q_out", d_q_out, torch.bfloat16, (T, hq, d), dev)
     _want(what, "d_k_out", d_k_out, torch.bfloat16, (T, hkv, d), dev)
@@ -670,6 +701,8 @@ class PagedCache:
                 _bad(what, "block_sums need a block_size")
         self.tensors = (k, v, k_scale, v_scale, block_sums, page_table, seq_lens)
         self.device, self.nseq, self.hkv, self.d = dev, nseq, hkv, d
+        self._index = -1 if dev.index is None else dev.index
+        load_library()
         self.block_size = block_size if block_sums is not None else 0
         ptr = [None if t is None else t.data_ptr() for t in self.tensors]
         self._c = _CacheStruct(*ptr, 1 if fp8 else 0, nseq, page_table.shape[1], pages, page, hkv,
@@ -705,6 +738,10 @@ def moba_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor,
     (cu_seqlens_q [nseq + 1]; cache.seq_lens already counts them) into the cache's pages, rounded
     to 8 bits where the cache is e4m3, and adds the keys to their blocks' sums."""
     what = "moba_cache_append"
+    if stream is None and _bind is not None and type(cache) is PagedCache:
+        done = _bind.append(cache._ref, cache._index, k, v, cu_seqlens_q)
+        if done is not None:
+            return _check(done, what)
     dev = _cache(what, cache)._here(what)
     k_ld = _rows(what, "k", k, cache.hkv, cache.d)
     v_ld = _rows(what, "v", v, cache.hkv, cache.d)
@@ -726,9 +763,13 @@ def moba_cache_read(cache: PagedCache, cu_seqlens: torch.Tensor, cu_seqlens_host
     as moba_attn_fwd takes them."""
     what = "moba_cache_read"
     dev = _cache(what, cache)._here(what)
-    _want(what, "cu_seqlens", cu_seqlens, torch.int32, (cache.nseq + 1,), dev)
     if len(cu_seqlens_host) != cache.nseq + 1:
         _bad(what, f"cu_seqlens_host must have {cache.nseq + 1} entries")
+    if stream is None and _bind is not None:
+        done = _bind.read(cache._ref, cache._index, cu_seqlens, int(cu_seqlens_host[-1]), k, v)
+        if done is not None:
+            return _done(done, what)
+    _want(what, "cu_seqlens", cu_seqlens, torch.int32, (cache.nseq + 1,), dev)
     shape = (int(cu_seqlens_host[-1]), cache.hkv, cache.d)
     if shape[0] < 0:
         _bad(what, "cu_seqlens_host must not be negative")
@@ -739,6 +780,16 @@ def moba_cache_read(cache: PagedCache, cu_seqlens: torch.Tensor, cu_seqlens_host
     _check(load_library().moba_cache_read(cache._ref, cu_seqlens.data_ptr(), shape[0],
                                           k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev)), what)
     return k, v
+
+
+def _paged_plain(cache, q, rows_per_seq, topk, scale, idx, o, lse, workspace, stream):
+    """The call through csrc/bind.cpp, or None where its arguments are not plain."""
+    if (stream is not None or _bind is None or type(cache) is not PagedCache
+            or not torch.is_tensor(q) or q.dim() != 3):
+        return None
+    nbytes = 0 if workspace is not None else cache.workspace_bytes(q.shape[1], rows_per_seq, topk)
+    return _bind.paged(cache._ref, cache._index, q, rows_per_seq, topk, scale, idx, o, lse,
+                       workspace, nbytes)
 
 
 def _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace, stream):
@@ -774,10 +825,15 @@ def moba_paged_attn_fwd(cache: PagedCache, q: torch.Tensor, rows_per_seq: int = 
     """Full attention of the last rows_per_seq tokens of every cached sequence: q
     [nseq * rows_per_seq, Hq, d] bf16; returns (o like q, lse [Hq, rows] fp32)."""
     what = "moba_paged_attn_fwd"
+    if scale is None:
+        scale = _cache(what, cache).d ** -0.5
+    done = _paged_plain(cache, q, rows_per_seq, 0, scale, None, o, lse, workspace, stream)
+    if done is not None:
+        return _done(done, what)
     dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, 0, o, lse, workspace, stream)
     st = load_library().moba_paged_attn_fwd(
-        cache._ref, q.data_ptr(), hq, rows_per_seq, cache.d ** -0.5 if scale is None else scale,
-        o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+        cache._ref, q.data_ptr(), hq, rows_per_seq, scale, o.data_ptr(),
+        lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     _check(st, what)
     return o, lse
 
@@ -793,12 +849,17 @@ def moba_paged_decode_fwd(cache: PagedCache, q: torch.Tensor, topk: int, rows_pe
     what = "moba_paged_decode_fwd"
     if topk < 1 or not _cache(what, cache).block_size:
         _bad(what, "topk must be positive and the cache have block_sums")
+    if scale is None:
+        scale = cache.d ** -0.5
+    done = _paged_plain(cache, q, rows_per_seq, topk, scale, block_idx_out, o, lse, workspace,
+                        stream)
+    if done is not None:
+        return _done(done, what)
     dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace, stream)
     if block_idx_out is not None and not _is(block_idx_out, torch.int32, (hq, n, topk), dev):
         _want(what, "block_idx_out", block_idx_out, torch.int32, (hq, n, topk), dev)
     st = load_library().moba_paged_decode_fwd(
-        cache._ref, q.data_ptr(), hq, rows_per_seq, topk,
-        cache.d ** -0.5 if scale is None else scale,
+        cache._ref, q.data_ptr(), hq, rows_per_seq, topk, scale,
         None if block_idx_out is None else block_idx_out.data_ptr(), o.data_ptr(), lse.data_ptr(),
         ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     _check(st, what)
