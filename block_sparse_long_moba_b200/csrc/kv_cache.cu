@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "sm100.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -32,35 +33,70 @@ namespace moba {
 namespace {
 
 constexpr int kCacheThreads = 256;
+constexpr int kAppendStages = 5;  // 40 KB a CTA, four CTAs an SM
+constexpr int kAppendSmem = kAppendStages * 2 * kCacheThreads * 16;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+// Packed arithmetic: an 8-bit row costs about as many instructions as HBM has clocks for it, so
+// maxima are taken on bf16 pairs as loaded and sums and products go two to an instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+struct Row8 {
+  float2 p[4];
+};
+__device__ __forceinline__ Row8 unpack8(const uint4& u) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  Row8 x;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = __uint_as_float(w[e] << 16);
-    x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-  }
+  for (int e = 0; e < 4; ++e)
+    x.p[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+  return x;
 }
 
-// Scale byte of a row whose largest magnitude is amax (448 = 1.75 * 2^8).
-__device__ __forceinline__ int scale_byte(float amax) {
-  const uint32_t u = __float_as_uint(amax);
-  const int b = static_cast<int>(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return max(b, 1);
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0 bytes read: the destination is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
 }
 
-__device__ __forceinline__ uint2 to_e4m3(const float (&x)[8], int b) {
-  const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);
-  uint32_t w[2];
+// Largest magnitude of eight bf16 as bf16 bits: without its sign a float orders as an integer.
+__device__ __forceinline__ uint32_t max_magnitude(const uint4& u) {
+  const uint32_t m = max_u16x2(max_u16x2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                              max_u16x2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+
+// Scale byte of a row whose largest magnitude has the bf16 bits m (448 = 1.75 * 2^8).
+__device__ __forceinline__ int scale_byte(uint32_t m) {
+  return max(static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u ? 1 : 0), 1);
+}
+
+__device__ __forceinline__ uint2 to_e4m3(const Row8& x, int b) {
+  const float f = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);
+  const float2 inv = make_float2(f, f);
+  uint32_t w[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-        make_float2(x[4 * h] * inv, x[4 * h + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-        make_float2(x[4 * h + 2] * inv, x[4 * h + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-    w[h] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-  }
-  return make_uint2(w[0], w[1]);
+  for (int e = 0; e < 4; ++e)
+    w[e] = __nv_cvt_float2_to_fp8x2(mul2(x.p[e], inv), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
 }
 
 struct CacheView {
@@ -99,11 +135,11 @@ __device__ __forceinline__ int last_not_above(int n, int x, F key) {
 __device__ __forceinline__ int first_unit(int cuq_s, int s, int B) { return cuq_s / B + 2 * s; }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kCacheThreads, 3) cache_append_kernel(const AppendArgs A) {
+__global__ void __launch_bounds__(kCacheThreads, 4) cache_append_kernel(const AppendArgs A) {
   constexpr int LPR = D / 8;               // lanes per row
   constexpr int SLOTS = kCacheThreads / LPR;
-  constexpr int U = 4;                     // rows in flight per lane group
   __shared__ float red[SLOTS][D];          // column sums per slot, then per head in red[head]
+  extern __shared__ __align__(128) uint8_t ring[];  // [kAppendStages][K, V][threads] x 16 bytes
   const CacheView& C = A.C;
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = static_cast<int>(cluster.num_blocks());
@@ -133,67 +169,70 @@ __global__ void __launch_bounds__(kCacheThreads, 3) cache_append_kernel(const Ap
   const int hh = slot % A.heads, tt = slot / A.heads;
   const bool mine = hh < nh && tt < TP;
   const int g = g0 + hh;
-  float sum[8];
+  Row8 sum;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  for (int e = 0; e < 4; ++e) sum.p[e] = make_float2(0.f, 0.f);
   const int mask = (1 << C.page_log) - 1;
-  for (int u = a0; u < a1; u += U * TP) {  // uniform over the CTA: shuffles below
-    uint4 kr[U], vr[U];
-    int pid[U];
+  // A thread's 16 bytes of K and V of its slot's rows a0 + tt, a0 + tt + TP, ... pass through a ring
+  // that it alone reads, kAppendStages - 1 rows ahead; no barrier.
+  const int iters = (a1 - a0 + TP - 1) / TP;  // uniform over the CTA: shuffles below
+  const uint32_t my_ring = smem_u32(ring) + threadIdx.x * 16;
+  const __nv_bfloat16* ksrc = A.k + (c0 + (a0 + tt - (L - n))) * A.k_ld + g * D + l * 8;
+  const __nv_bfloat16* vsrc = A.v + (c0 + (a0 + tt - (L - n))) * A.v_ld + g * D + l * 8;
+  const long long k_step = TP * A.k_ld, v_step = TP * A.v_ld;
+  int ahead = a0 + tt;  // row of the next copy
+  auto issue = [&](int stage) {
+    const bool in = mine && ahead < a1;
+    const uint32_t d = my_ring + stage * (2 * kCacheThreads * 16);
+    copy16(d, in ? ksrc : A.k, in);
+    copy16(d + kCacheThreads * 16, in ? vsrc : A.v, in);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead += TP;
+    ksrc += k_step;
+    vsrc += v_step;
+  };
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int x = u + i * TP + tt;
-      const bool in = mine && x < a1;
-      const long long row = c0 + (x - (L - n));
-      kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-      pid[i] = -1;
-      if (in) {
-        kr[i] = __ldcs(reinterpret_cast<const uint4*>(A.k + row * A.k_ld + g * D) + l);
-        vr[i] = __ldcs(reinterpret_cast<const uint4*>(A.v + row * A.v_ld + g * D) + l);
-        pid[i] = __ldg(pages + (x >> C.page_log));
+  for (int i = 0; i < kAppendStages - 1; ++i) issue(i);
+  int x = a0 + tt, stage = 0;
+  auto page_of = [&](int u) { return mine && u < a1 ? __ldg(pages + (u >> C.page_log)) : -1; };
+  int pid = page_of(x);
+  for (int it = 0; it < iters; ++it, x += TP) {
+    issue(stage == 0 ? kAppendStages - 1 : stage - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAppendStages - 1) : "memory");
+    const uint8_t* from = ring + stage * (2 * kCacheThreads * 16) + threadIdx.x * 16;
+    const uint4 kr = *reinterpret_cast<const uint4*>(from);
+    const uint4 vr = *reinterpret_cast<const uint4*>(from + kCacheThreads * 16);
+    stage = stage + 1 == kAppendStages ? 0 : stage + 1;
+    const bool ok = pid >= 0 && pid < C.num_pages;  // false when the row is not ours
+    const size_t at = ((static_cast<size_t>(ok ? pid : 0) * C.G + g) << C.page_log) + (x & mask);
+    pid = page_of(x + TP);
+    const Row8 kx = unpack8(kr);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum.p[e] = sum2(sum.p[e], kx.p[e]);
+    if (FP8) {
+      // both maxima in one butterfly: the key row's in the low half, the value row's in the high
+      uint32_t top = max_magnitude(kr) | max_magnitude(vr) << 16;
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1)
+        top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int kb = scale_byte(top & 0xffffu), vb = scale_byte(top >> 16);
+      if (ok) {
+        *reinterpret_cast<uint2*>(C.k + at * D + l * 8) = to_e4m3(kx, kb);
+        *reinterpret_cast<uint2*>(C.v + at * D + l * 8) = to_e4m3(unpack8(vr), vb);
+        if (l == 0) {
+          C.ks[at] = static_cast<uint8_t>(kb);
+          C.vs[at] = static_cast<uint8_t>(vb);
+        }
       }
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int x = u + i * TP + tt;
-      const bool ok = pid[i] >= 0 && pid[i] < C.num_pages;  // false when the row is not ours
-      const size_t at = ((static_cast<size_t>(ok ? pid[i] : 0) * C.G + g) << C.page_log) +
-                        (x & mask);
-      float kx[8], vx[8];
-      unpack8(kr[i], kx);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += kx[e];
-      if (FP8) {
-        unpack8(vr[i], vx);
-        float ka = 0.f, va = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ka = fmaxf(ka, fabsf(kx[e]));
-          va = fmaxf(va, fabsf(vx[e]));
-        }
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) {
-          ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
-          va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
-        }
-        const int kb = scale_byte(ka), vb = scale_byte(va);
-        if (ok) {
-          *reinterpret_cast<uint2*>(C.k + at * D + l * 8) = to_e4m3(kx, kb);
-          *reinterpret_cast<uint2*>(C.v + at * D + l * 8) = to_e4m3(vx, vb);
-          if (l == 0) {
-            C.ks[at] = static_cast<uint8_t>(kb);
-            C.vs[at] = static_cast<uint8_t>(vb);
-          }
-        }
-      } else if (ok) {
-        *reinterpret_cast<uint4*>(C.k + (at * D + l * 8) * 2) = kr[i];
-        *reinterpret_cast<uint4*>(C.v + (at * D + l * 8) * 2) = vr[i];
-      }
+    } else if (ok) {
+      *reinterpret_cast<uint4*>(C.k + (at * D + l * 8) * 2) = kr;
+      *reinterpret_cast<uint4*>(C.v + (at * D + l * 8) * 2) = vr;
     }
   }
   if (!C.sums) return;  // uniform over the grid
 #pragma unroll
-  for (int e = 0; e < 8; ++e) red[slot][l * 8 + e] = mine ? sum[e] : 0.f;
+  for (int e = 0; e < 8; ++e)
+    red[slot][l * 8 + e] = mine ? (e & 1 ? sum.p[e >> 1].y : sum.p[e >> 1].x) : 0.f;
   __syncthreads();
   // red[h] <- sum over the row slots of head h, slots in order
   for (int x = threadIdx.x; x < nh * D; x += kCacheThreads) {
@@ -338,12 +377,13 @@ cudaError_t append(const PagedCache& P, AppendArgs A, int sms, cudaStream_t s) {
   // CTA has several passes of rows to write, fewer while the grid would not fill the SMs.
   int heads = std::min(P.G, SLOTS);
   const long long busy = std::max<long long>(1, A.Tq / B + P.nseq) * cs;
-  while (heads > 1 && rows / cs > 8 && busy * ((P.G + heads - 1) / heads) < 4ll * sms)
+  while (heads > 1 && rows / cs > 8 && busy * ((P.G + heads - 1) / heads) < 12ll * sms)
     heads = (heads + 1) / 2;
   A.heads = heads;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * cs), (P.G + heads - 1) / heads);
   cfg.blockDim = dim3(kCacheThreads);
+  cfg.dynamicSmemBytes = kAppendSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
