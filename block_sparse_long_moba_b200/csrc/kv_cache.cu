@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kCacheThreads, 4) cache_append_kernel(const Ap
   const int CS = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
   const int unit = blockIdx.x / CS;
+  wait_previous_kernel();
   const int s = last_not_above(C.nseq, unit, [&](int x) {
     return first_unit(__ldg(A.cuq + x), x, C.B);
   });
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const ReadArg
   const CacheView& C = A.C;
   const int r0 = blockIdx.x * kReadRows;
   const int nr = min(kReadRows, A.T - r0);
+  wait_previous_kernel();
   if (threadIdx.x < 32) {  // kReadRows rows, one per lane
     const int s0 = last_not_above(C.nseq, r0, [&](int x) { return __ldg(A.cu + x); });
     const int r = r0 + threadIdx.x;
@@ -380,18 +382,9 @@ cudaError_t append(const PagedCache& P, AppendArgs A, int sms, cudaStream_t s) {
   while (heads > 1 && rows / cs > 8 && busy * ((P.G + heads - 1) / heads) < 12ll * sms)
     heads = (heads + 1) / 2;
   A.heads = heads;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * cs), (P.G + heads - 1) / heads);
-  cfg.blockDim = dim3(kCacheThreads);
-  cfg.dynamicSmemBytes = kAppendSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(cs);
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_append_kernel<D, FP8>, A);
+  return launch_early(cache_append_kernel<D, FP8>,
+                      dim3(static_cast<unsigned>(units * cs), (P.G + heads - 1) / heads),
+                      kCacheThreads, kAppendSmem, cs, s, A);
 }
 
 }  // namespace
@@ -415,15 +408,10 @@ cudaError_t launch_cache_read(const PagedCache& P, void* k, void* v, const int32
   A.k = static_cast<__nv_bfloat16*>(k);
   A.v = static_cast<__nv_bfloat16*>(v);
   A.cu = cu; A.T = T;
-  const unsigned grid = (T + kReadRows - 1) / kReadRows;
-  if (P.d == 64) {
-    if (P.fp8) cache_read_kernel<64, true><<<grid, kCacheThreads, 0, s>>>(A);
-    else cache_read_kernel<64, false><<<grid, kCacheThreads, 0, s>>>(A);
-  } else {
-    if (P.fp8) cache_read_kernel<128, true><<<grid, kCacheThreads, 0, s>>>(A);
-    else cache_read_kernel<128, false><<<grid, kCacheThreads, 0, s>>>(A);
-  }
-  return cudaGetLastError();
+  const dim3 grid((T + kReadRows - 1) / kReadRows);
+  auto kernel = P.d == 64 ? (P.fp8 ? cache_read_kernel<64, true> : cache_read_kernel<64, false>)
+                          : (P.fp8 ? cache_read_kernel<128, true> : cache_read_kernel<128, false>);
+  return launch_early(kernel, grid, kCacheThreads, 0, 1, s, A);
 }
 
 }  // namespace moba

@@ -167,6 +167,36 @@ cudaError_t launch_bwd_finish(const BwdLaunch& L, cudaStream_t stream);
 // SMs of a B200: sizes the grids and workspaces below without a device query.
 constexpr int kNumSms = 148;
 
+// Launch whose CTAs may be scheduled while the kernel before it on the stream drains: the kernel
+// calls wait_previous_kernel() before it reads or writes anything, so that the order of the stream
+// is kept and only the launch latency is hidden. cluster: CTAs of a cluster along x.
+template <class... K, class... A>
+cudaError_t launch_early(void (*kernel)(K...), dim3 grid, int block, size_t smem, int cluster,
+                         cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+// The kernel before this one on the stream may still run: wait for its results. Its counterpart
+// lets the next kernel's CTAs be scheduled.
+__device__ __forceinline__ void wait_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void allow_next_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Norm + rotary position of q and k, and its gradients (csrc/qk_norm.cu).
 struct NormLaunch {
   const void *q, *k;          // bf16 [T, Hq, d] and [T, Hkv, d], tokens q_ld / k_ld elements apart

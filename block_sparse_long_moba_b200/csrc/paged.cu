@@ -132,15 +132,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// The kernel before this one on the stream may still run (programmatic launch): wait for its
-// results before the first read of them; let the next kernel's CTAs be scheduled early.
-__device__ __forceinline__ void wait_previous_kernel() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void allow_next_kernel() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ---------------------------------------------------------------------------------- arguments
 struct PagedArgs {
   const __nv_bfloat16* q;  // [nseq * rows, Hq, D]
@@ -231,7 +222,7 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = lane & 3, n4 = lane >> 2;
   allow_next_kernel();
-  if (SPARSE) wait_previous_kernel();
+  wait_previous_kernel();
 
   // Tiles of one segment.
   auto tiles_of = [&](int seg) -> int {
@@ -808,9 +799,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
   const int s = row / A.rows, r = row % A.rows, g = h / A.group;
   const int rr = r * A.group + h % A.group, rt = rr / kRows, col = rr % kRows;
   const int seg = (s * A.G + g) * A.nrt + rt;
+  wait_previous_kernel();
   bool over;
   const int L = seq_len(A, s, &over);
-  wait_previous_kernel();
   // written for every segment that has tiles
   const int2 desc = A.seg_desc[seg];
   const int tiles = sparse ? A.seg_tiles[seg] : L;
@@ -1003,6 +994,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
   const int seg = blockIdx.x / CS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   allow_next_kernel();
+  wait_previous_kernel();
   const Seg id = seg_of(A, seg);
   const int R = A.rows * A.group, row0 = id.rt * kRows;
   const int nrow = min(kRows, R - row0);  // rows of this tile (<= RR)
@@ -1383,17 +1375,9 @@ cudaError_t attn(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
   constexpr int smem = Tile<D, FP8>::kWarps * Tile<D, FP8>::kWarpBytes;
   cudaError_t e = allow_smem(paged_attn_kernel<D, FP8, NT, SPARSE>, smem, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(L.shape.ctas));
-  cfg.blockDim = dim3(Tile<D, FP8>::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = SPARSE ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, FP8, NT, SPARSE>, A);
+  return launch_early(paged_attn_kernel<D, FP8, NT, SPARSE>,
+                      dim3(static_cast<unsigned>(L.shape.ctas)), Tile<D, FP8>::kThreads, smem, 1, s,
+                      A);
 }
 
 template <int D, int RR>
@@ -1403,34 +1387,19 @@ cudaError_t gate(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
   const size_t smem = in_smem ? static_cast<size_t>(A.nb_cap) * (RR * 8 + 4) : 0;
   cudaError_t e = allow_smem(paged_gate_kernel<D, RR>, kGateSmem, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(A.nseg) * L.shape.gate_ctas);
-  cfg.blockDim = dim3(kGateThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(L.shape.gate_ctas);
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   const int kt = tile_bytes(L.cache.fp8) / (D * (L.cache.fp8 ? 1 : 2));
-  return cudaLaunchKernelEx(&cfg, paged_gate_kernel<D, RR>, A, L.shape.rows_per_tile, kt, in_smem);
+  return launch_early(paged_gate_kernel<D, RR>,
+                      dim3(static_cast<unsigned>(A.nseg) * L.shape.gate_ctas), kGateThreads, smem,
+                      L.shape.gate_ctas, s, A, L.shape.rows_per_tile, kt, in_smem);
 }
 
 template <int D>
 cudaError_t merge(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(A.nseq) * A.rows * A.Hq);
   // a segment has about ctas * warps / nseg + 1 partials
-  cfg.blockDim = dim3(32 * (A.nseg >= 512 ? 2 : A.nseg >= 128 ? 4 : kMergeWarps));
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, A, L.shape.rows_per_tile, L.topk > 0);
+  const int warps = A.nseg >= 512 ? 2 : A.nseg >= 128 ? 4 : kMergeWarps;
+  return launch_early(paged_merge_kernel<D>,
+                      dim3(static_cast<unsigned>(A.nseq) * A.rows * A.Hq), 32 * warps, 0, 1, s, A,
+                      L.shape.rows_per_tile, L.topk > 0);
 }
 
 }  // namespace

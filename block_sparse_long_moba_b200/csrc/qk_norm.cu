@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_rope_kernel(const Nor
   if (!isq) chunk -= A.qchunks;
   const int H = isq ? A.Hq : A.Hkv, h0 = chunk * chunk_rows(D) + sub;
   const Place<ADJ> P(l, A.rot);
+  wait_previous_kernel();
   Elems acc;
 #pragma unroll
   for (int e = 0; e < 2; ++e) acc.a[e] = acc.b[e] = make_float2(0.f, 0.f);
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* __restric
                                                           float* __restrict__ dwk) {
   __shared__ double red[32][33];
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5, x = blockIdx.x * 32 + c;
+  wait_previous_kernel();
   double s = 0.;
 #pragma unroll 20
   for (int i = w; i < n; i += 32)
@@ -441,8 +443,8 @@ cudaError_t launch(const NormArgs& A, int ctas, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_relaxed);
   }
-  qk_norm_rope_kernel<D, ADJ, BWD><<<ctas, kNormThreads, norm_smem(BWD), s>>>(A);
-  return cudaGetLastError();
+  return launch_early(qk_norm_rope_kernel<D, ADJ, BWD>, dim3(static_cast<unsigned>(ctas)),
+                      kNormThreads, norm_smem(BWD), 1, s, A);
 }
 
 template <bool BWD>
@@ -474,8 +476,7 @@ cudaError_t launch_qk_norm_bwd(const NormLaunch& L, int ctas, cudaStream_t s) {
 
 cudaError_t launch_qk_norm_dw(const float* part, int n, int d, float* dwq, float* dwk,
                               cudaStream_t s) {
-  qk_norm_dw_kernel<<<2 * d / 32, 1024, 0, s>>>(part, n, d, dwq, dwk);
-  return cudaGetLastError();
+  return launch_early(qk_norm_dw_kernel, dim3(2 * d / 32), 1024, 0, 1, s, part, n, d, dwq, dwk);
 }
 
 }  // namespace moba
