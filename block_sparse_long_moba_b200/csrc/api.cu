@@ -964,7 +964,7 @@ int paged_run(const moba_paged_cache* c, const void* q, int Hq, int rows, int to
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (topk) MOBA_LAUNCH_NAMED(kDecode, "moba_paged_gate", s, launch_paged_gate(D, s));
   MOBA_LAUNCH_NAMED(kDecode, "moba_paged_attn", s, launch_paged_attn(D, s));
-  MOBA_LAUNCH_NAMED(kDecode, "moba_paged_merge", s, launch_paged_merge(D, s));
+  if (!D.shape.join) MOBA_LAUNCH_NAMED(kDecode, "moba_paged_merge", s, launch_paged_merge(D, s));
   return MOBA_OK;
 }
 

@@ -237,6 +237,7 @@ struct PagedShape {
   int rows_per_tile, nrt;  // rows of a segment (8 or 16), row tiles per (sequence, kv head)
   long long nseg, slots;   // segments, partial results
   int ctas;                // of the attention kernel
+  int join;                // CTAs of a cluster per segment, 0: segments share the grid, then a merge
   int nb_cap, ent_cap;     // blocks of a full sequence, selected blocks of a segment at most
   int gate_ctas;           // CTAs of one segment's gate
   bool gate_global;        // keys and marks of the gate in the workspace

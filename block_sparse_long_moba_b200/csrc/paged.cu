@@ -141,6 +141,7 @@ struct PagedArgs {
   int nseq, max_pages, num_pages, page_log, G, B;
   int rows, Hq, group, nrt, nseg;  // nrt row tiles per (sequence, kv head); nseg segments
   int topk, nb_cap, ent_cap, tiles_per_block;
+  int join;  // CTAs of the cluster that has one segment to itself; 0: all segments on one line
   float scale_log2;
   // workspace
   int2* seg_desc;        // [nseg] first worker of a segment, its workers (1: written directly)
@@ -230,6 +231,17 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
     bool over;
     return (seq_len(A, seg / (A.G * A.nrt), &over) + KT - 1) / KT;
   };
+  int workers, me, seg0 = 0;
+  long long U, ub, ue, seg_begin = 0;
+  if (A.join) {  // this cluster's segment, split over its warps
+    seg0 = blockIdx.x / A.join;
+    U = tiles_of(seg0);
+    workers = static_cast<int>(min(static_cast<long long>(A.join) * kPagedWarps, U));
+    // neighbouring tiles go to different CTAs, so that few tiles still use all of them
+    me = warp * A.join + static_cast<int>(blockIdx.x % A.join);
+    ub = me < workers ? range_start(U, me, workers) : 0;
+    ue = me < workers ? range_start(U, me + 1, workers) : 0;
+  } else {
   // Prefix sums: thread t owns a run of segments.
   const int per = (A.nseg + kPagedThreads - 1) / kPagedThreads;
   {
@@ -255,17 +267,15 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
     if (tid == 0) prefix[kPagedThreads] = all;
     __syncthreads();
   }
-  const long long U = prefix[kPagedThreads];
+  U = prefix[kPagedThreads];
   // Neighbouring workers sit on different SMs, so that few tiles still use many of them.
-  const int workers = static_cast<int>(
-      min(static_cast<long long>(gridDim.x) * kPagedWarps, U));
-  const int me = warp * gridDim.x + blockIdx.x;
-  if (me >= workers) return;  // no block-wide barrier below
-  const long long ub = range_start(U, me, workers), ue = range_start(U, me + 1, workers);
+  workers = static_cast<int>(min(static_cast<long long>(gridDim.x) * kPagedWarps, U));
+  me = warp * gridDim.x + blockIdx.x;
+  if (me >= workers) return;  // no block-wide barrier below on this path
+  ub = range_start(U, me, workers);
+  ue = range_start(U, me + 1, workers);
 
   // Segment of tile ub: the run that holds it, then 32 segments at a time.
-  int seg0 = 0;
-  long long seg_begin = 0;
   {
     int run = 0;
     for (int x = lane; x < kPagedThreads; x += 32)
@@ -291,6 +301,7 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
       }
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
+  }
   }
 
   uint8_t* wbase = smem + warp * TL::kWarpBytes;
@@ -489,10 +500,14 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
   };
 
   auto finish = [&](int sg, int t0, int t1) {  // this warp had tiles [t0, t1) of the segment
-    const bool whole = t0 == 0 && t1 == cur_tiles;
+    const bool whole = t0 == 0 && t1 == cur_tiles && !A.join;
     const int R = A.rows * A.group;
     const size_t slot = static_cast<size_t>(me) + sg;
-    if (t1 == cur_tiles && lane == 0) {
+    // partials: in the workspace, or in this warp's own (now idle) ring for the cluster to join
+    float* po = A.join ? reinterpret_cast<float*>(wbase) : A.part_o + slot * kRows * D;
+    float2* pml = A.join ? reinterpret_cast<float2*>(wbase + kRows * D * 4)
+                         : A.part_ml + slot * kRows;
+    if (t1 == cur_tiles && lane == 0 && !A.join) {
       int w0 = me;
       if (!whole) {  // worker of the segment's first tile
         w0 = static_cast<int>(cur_begin * workers / U);
@@ -535,14 +550,14 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
             A.lse[static_cast<size_t>(h) * A.nseq * A.rows + row] =
                 bad ? nan : s > 0.f ? (top + log2f(s)) * 0.69314718055994531f : -INFINITY;
         } else {
-          float* dst = A.part_o + (slot * kRows + col) * D;
+          float* dst = po + col * D;
 #pragma unroll
           for (int ds = 0; ds < KS; ++ds) {
             const int d0 = ds * 16 + (FP8 ? 2 * n4 : n4), d1 = d0 + (FP8 ? 1 : 8);
             dst[d0] = acc[ds][nt][j] * mul;
             dst[d1] = acc[ds][nt][2 + j] * mul;
           }
-          if (n4 == 0) A.part_ml[slot * kRows + col] = make_float2(top, s);
+          if (n4 == 0) pml[col] = make_float2(top, s);
         }
       }
   };
@@ -777,7 +792,104 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   cp_async_wait<0>();
+  if (A.join) __syncwarp();  // all copies into the ring have landed: it takes the partial
   if (seg >= 0) finish(seg, first_tile_of_seg, next_tile);
+  if (!A.join) return;
+
+  // ---- the cluster joins its segment. CTA r takes rows r, r + CTAs, ...: a warp per row and slice
+  // of the partials, lanes over d, eight partials in flight; the slices meet in shared memory.
+  float2* my_ml = reinterpret_cast<float2*>(wbase + kRows * D * 4);
+  if (seg < 0 && lane < kRows) my_ml[lane] = make_float2(-INFINITY, 0.f);
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  constexpr int PER = D / 32;
+  float* slices = reinterpret_cast<float*>(smem + kRows * D * 4 + kRows * 8);  // [warps][D]
+  const Seg js = seg_of(A, seg0);
+  bool over;
+  seq_len(A, js.s, &over);
+  if (SPARSE) over |= A.seg_tiles[seg0] < 0;
+  const int crank = blockIdx.x % A.join;
+  const int nrow = min(kRows, A.rows * A.group - js.rt * kRows);
+  const int mine = (nrow - crank + A.join - 1) / A.join;  // rows of this CTA
+  int nr = 1;  // rows at once
+  while (nr < mine && nr < kPagedWarps) nr *= 2;
+  const int parts = A.join * kPagedWarps;  // at most 64, two to a lane
+  const int nslice = kPagedWarps / nr, each = parts / nslice, slice = warp / nr;
+  for (int k0 = 0; k0 < mine; k0 += nr) {  // uniform over the CTA
+    const int k = k0 + warp % nr, row = crank + k * A.join;
+    const bool on = k < mine;
+    auto part = [&](int i) {  // partial i in the memory of its CTA
+      return cluster.map_shared_rank(smem + (i / A.join) * TL::kWarpBytes, i % A.join);
+    };
+    float pm[2], pl[2], top = -INFINITY, sum = 0.f, o[PER];
+    bool nan = over;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      pm[h] = -INFINITY;
+      pl[h] = 0.f;
+      if (on && h * 32 + lane < parts) {
+        const float2 ml =
+            reinterpret_cast<const float2*>(part(h * 32 + lane) + kRows * D * 4)[row];
+        pm[h] = ml.x;
+        pl[h] = ml.y;
+      }
+      nan |= !(pm[h] <= FLT_MAX);
+      top = fmaxf(top, pm[h]);
+    }
+    nan = __any_sync(0xffffffffu, nan);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      pl[h] = pl[h] > 0.f ? pl[h] * ex2(pm[h] - top) : 0.f;
+      sum += pl[h];
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    for (int i0 = slice * each; i0 < (slice + 1) * each; i0 += 8) {
+      float w[8], v[8][PER];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = min(i0 + i, parts - 1);
+        const float w0 = __shfl_sync(0xffffffffu, pl[0], at & 31);
+        const float w1 = __shfl_sync(0xffffffffu, pl[1], at & 31);
+        w[i] = i0 + i >= (slice + 1) * each ? 0.f : at < 32 ? w0 : w1;
+        const float* src = reinterpret_cast<const float*>(part(at)) + row * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[i][e] = on ? src[e] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < PER; ++e)  // a warp without tiles has left no values
+          o[e] = w[i] > 0.f ? fmaf(w[i], v[i][e], o[e]) : o[e];
+    }
+    if (nslice > 1) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) slices[warp * D + lane * PER + e] = o[e];
+      __syncthreads();
+      if (slice == 0)
+        for (int x = 1; x < nslice; ++x)
+#pragma unroll
+          for (int e = 0; e < PER; ++e) o[e] += slices[(x * nr + warp) * D + lane * PER + e];
+    }
+    if (slice == 0 && on) {
+      const int rr = js.rt * kRows + row, h = js.g * A.group + rr % A.group;
+      const size_t at = static_cast<size_t>(js.s) * A.rows + rr / A.group;
+      const float inv = nan ? __int_as_float(0x7fffffff) : sum > 0.f ? 1.f / sum : 0.f;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(A.o + (at * A.Hq + h) * D + lane * PER);
+#pragma unroll
+      for (int e = 0; e < PER; e += 2)
+        dst[e / 2] = nan ? 0x7fff7fffu : pack_bf16(o[e] * inv, o[e + 1] * inv);
+      if (lane == 0)
+        A.lse[static_cast<size_t>(h) * A.nseq * A.rows + at] =
+            nan ? inv : sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    }
+    if (nslice > 1) __syncthreads();  // slices before the next rows
+  }
+  cluster.sync();  // peers' partials stay until everyone has read them
 }
 
 // ------------------------------------------------------------------------------------- merge
@@ -995,6 +1107,9 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   allow_next_kernel();
   wait_previous_kernel();
+  auto sync_all = [&]() {  // the segment's CTAs
+    if (CS > 1) cluster.sync(); else __syncthreads();
+  };
   const Seg id = seg_of(A, seg);
   const int R = A.rows * A.group, row0 = id.rt * kRows;
   const int nrow = min(kRows, R - row0);  // rows of this tile (<= RR)
@@ -1082,7 +1197,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
       }
     }
   }
-  cluster.sync();
+  sync_all();
 
   // ---- selection. select(row, where) writes its results through these.
   int2* ent = A.entries + static_cast<size_t>(seg) * A.ent_cap;
@@ -1290,7 +1405,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
       __syncthreads();  // shared arrays before the next row
     }
   }
-  if (RR > 1) cluster.sync();  // all rows' marks
+  if (RR > 1) sync_all();      // all rows' marks
   else __syncthreads();        // stot (rank 0 has the one row)
   if (rank == 0) {  // the blocks that a row selected, ascending
     bool bad = over;
@@ -1344,6 +1459,7 @@ PagedArgs args_of(const PagedLaunch& L) {
   A.topk = L.topk; A.nb_cap = L.shape.nb_cap; A.ent_cap = L.shape.ent_cap;
   const int kt = tile_bytes(P.fp8) / (P.d * (P.fp8 ? 1 : 2));
   A.tiles_per_block = L.topk ? (P.B + kt - 1) / kt : 0;
+  A.join = L.shape.join;
   A.scale_log2 = L.scale * 1.4426950408889634f;
   A.seg_desc = reinterpret_cast<int2*>(L.seg_desc);
   A.part_o = L.part_o; A.part_ml = reinterpret_cast<float2*>(L.part_ml);
@@ -1376,8 +1492,8 @@ cudaError_t attn(const PagedArgs& A, const PagedLaunch& L, cudaStream_t s) {
   cudaError_t e = allow_smem(paged_attn_kernel<D, FP8, NT, SPARSE>, smem, done);
   if (e != cudaSuccess) return e;
   return launch_early(paged_attn_kernel<D, FP8, NT, SPARSE>,
-                      dim3(static_cast<unsigned>(L.shape.ctas)), Tile<D, FP8>::kThreads, smem, 1, s,
-                      A);
+                      dim3(static_cast<unsigned>(A.join ? A.nseg * A.join : L.shape.ctas)),
+                      Tile<D, FP8>::kThreads, smem, A.join ? A.join : 1, s, A);
 }
 
 template <int D, int RR>
@@ -1416,6 +1532,7 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
   const long long tiles = S.nseg * ((cap + kt - 1) / kt);
   S.ctas = static_cast<int>(std::min<long long>(sms, (tiles + warps - 1) / warps));
   S.slots = static_cast<long long>(S.ctas) * warps + S.nseg;
+  long long seg_tiles = (cap + kt - 1) / kt;  // of a segment at most
   if (topk) {
     S.nb_cap = static_cast<int>((cap + P.B - 1) / P.B);
     S.ent_cap = static_cast<int>(std::min<long long>(
@@ -1426,8 +1543,26 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
     while (S.gate_ctas < 8 && S.nb_cap > 64 * S.gate_ctas &&
            S.nseg * S.gate_ctas * 2 <= 2 * kNumSms)
       S.gate_ctas *= 2;
+    seg_tiles = std::min(seg_tiles, static_cast<long long>(S.ent_cap) * ((P.B + kt - 1) / kt));
     const int rr = std::min(R, S.rows_per_tile);
     S.gate_global = S.gate_ctas > 1 || static_cast<long long>(S.nb_cap) * (rr * 16 + 4) > kGateSmem;
+  }
+  // Few and short segments: a cluster has each to itself and joins it in its own memory, one launch
+  // instead of two. Only while all clusters run at once, and while a warp then has little more to do
+  // than with the tiles spread over every SM: a bf16 tile takes a warp about 1 us, the merge kernel
+  // 3; e4m3 tiles take longer and their 8 warps make more partials, so its margin is smaller and its
+  // clusters at most two. Measured, d = 128, 32 / 8 heads, joined against spread and merged:
+  // 16 x 500 tokens 10 us : 15 (either type), 1 x 4000 bf16 11.8 : 13.0, 1 x 8000 bf16 (4.4 tiles
+  // more per warp) 15.2 : 15.0, 4 x 1000 e4m3 (1.1 more) 12.4 : 11.8.
+  if (S.nseg <= sms) {
+    const int most = P.fp8 ? 2 : 8;
+    const double margin = P.fp8 ? 0.75 : 3.0;
+    int cs = 1;
+    while (cs < most && S.nseg * cs * 2 <= sms && seg_tiles > static_cast<long long>(cs) * warps)
+      cs *= 2;
+    const double joined = static_cast<double>(seg_tiles) / (cs * warps);
+    const double spread = static_cast<double>(seg_tiles) * S.nseg / (sms * warps);
+    if (joined <= spread + margin) S.join = cs;
   }
   return S;
 }
