@@ -912,12 +912,12 @@ PagedLayout paged_layout(const PagedShape& S, int d, int topk) {
   const size_t nseg = static_cast<size_t>(S.nseg);
   const size_t rows = static_cast<size_t>(S.slots) * S.rows_per_tile;
   L.seg_desc = take(nseg * 8);
-  L.part_o = take(rows * d * 4);
-  L.part_ml = take(rows * 8);
+  L.part_o = take(S.join ? 0 : rows * d * 4);
+  L.part_ml = take(S.join ? 0 : rows * 8);
   L.seg_tiles = take(topk ? nseg * 4 : 0);
   L.entries = take(topk ? nseg * S.ent_cap * 8 : 0);
   const bool global = topk && S.gate_global;
-  L.keys = take(global ? nseg * S.rows_per_tile * S.nb_cap * 8 : 0);
+  L.keys = take(global ? nseg * S.gate_rows * S.nb_cap * 8 : 0);
   L.marks = take(global ? nseg * S.nb_cap * 4 : 0);
   L.total = o;
   return L;

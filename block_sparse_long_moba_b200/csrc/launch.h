@@ -235,6 +235,7 @@ cudaError_t launch_cache_read(const PagedCache& P, void* k, void* v, const int32
 
 struct PagedShape {
   int rows_per_tile, nrt;  // rows of a segment (8 or 16), row tiles per (sequence, kv head)
+  int gate_rows;           // of a segment's tile that hold a row: min(rows, rows_per_tile)
   long long nseg, slots;   // segments, partial results
   int ctas;                // of the attention kernel
   int join;                // CTAs of a cluster per segment, 0: segments share the grid, then a merge

@@ -145,11 +145,13 @@ struct PagedArgs {
   float scale_log2;
   // workspace
   int2* seg_desc;        // [nseg] first worker of a segment, its workers (1: written directly)
-  float* part_o;         // [slots][kRows][D]
-  float2* part_ml;       // [slots][kRows]
+  // partials, [2 workers][kRows]: worker w's of a segment that began before it at 2 w, of one that
+  // it begins and another finishes at 2 w + 1
+  float* part_o;         // x D
+  float2* part_ml;
   int* seg_tiles;        // sparse: [nseg] tiles, -1: a page outside the pool
   int2* entries;         // sparse: [nseg][ent_cap] (block, rows that selected it)
-  unsigned long long* keys;  // sparse: [nseg][kRows][nb_cap] order keys (large caches)
+  unsigned long long* keys;  // sparse: [nseg][rows of a tile][nb_cap] order keys (large caches)
   unsigned int* marks;       // sparse: [nseg][nb_cap] rows that selected a block (large caches)
   int32_t* idx;          // sparse, nullable: [Hq, nseq * rows, topk]
   __nv_bfloat16* o;
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
   auto finish = [&](int sg, int t0, int t1) {  // this warp had tiles [t0, t1) of the segment
     const bool whole = t0 == 0 && t1 == cur_tiles && !A.join;
     const int R = A.rows * A.group;
-    const size_t slot = static_cast<size_t>(me) + sg;
+    const size_t slot = 2 * static_cast<size_t>(me) + (t0 == 0 ? 1 : 0);
     // partials: in the workspace, or in this warp's own (now idle) ring for the cluster to join
     float* po = A.join ? reinterpret_cast<float*>(wbase) : A.part_o + slot * kRows * D;
     float2* pml = A.join ? reinterpret_cast<float2*>(wbase + kRows * D * 4)
@@ -923,7 +925,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
   float m = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  const size_t slot0 = static_cast<size_t>(desc.x) + seg;
   for (int i0 = warp; i0 < count; i0 += NW * kMergeBatch) {
     float2 ml[kMergeBatch];
     float o[kMergeBatch][PER];
@@ -934,7 +935,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
 #pragma unroll
       for (int e = 0; e < PER; ++e) o[x][e] = 0.f;
       if (i < count) {
-        const size_t at = (slot0 + i) * kRows + col;
+        const size_t at = (2 * static_cast<size_t>(desc.x + i) + (i == 0 ? 1 : 0)) * kRows + col;
         ml[x] = A.part_ml[at];
         const float* src = A.part_o + at * D + lane * PER;
         if constexpr (PER == 4) {
@@ -1135,7 +1136,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
   const int L = seq_len(A, id.s, &over);
   const int last = L > 0 ? (L - 1) / A.B : -1;  // current block of the newest row
   unsigned long long* keys =
-      in_smem ? skeys : A.keys + static_cast<size_t>(seg) * kRows * A.nb_cap;
+      in_smem ? skeys : A.keys + static_cast<size_t>(seg) * min(kRows, R) * A.nb_cap;
   unsigned int* marks = in_smem ? reinterpret_cast<unsigned int*>(skeys + RR * A.nb_cap)
                                 : A.marks + static_cast<size_t>(seg) * A.nb_cap;
   if (tid == 0) sbad = 0;
@@ -1525,13 +1526,14 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
   const int R = rows * (Hq / P.G);
   S.rows_per_tile = R <= 8 ? 8 : 16;
   S.nrt = (R + S.rows_per_tile - 1) / S.rows_per_tile;
+  S.gate_rows = std::min(R, S.rows_per_tile);
   S.nseg = static_cast<long long>(P.nseq) * P.G * S.nrt;
   const int kt = tile_bytes(P.fp8) / (P.d * (P.fp8 ? 1 : 2));
   const int warps = paged_warps(P.fp8);
   const long long cap = static_cast<long long>(P.max_pages) << P.page_log;
   const long long tiles = S.nseg * ((cap + kt - 1) / kt);
   S.ctas = static_cast<int>(std::min<long long>(sms, (tiles + warps - 1) / warps));
-  S.slots = static_cast<long long>(S.ctas) * warps + S.nseg;
+  S.slots = 2ll * S.ctas * warps;
   long long seg_tiles = (cap + kt - 1) / kt;  // of a segment at most
   if (topk) {
     S.nb_cap = static_cast<int>((cap + P.B - 1) / P.B);
@@ -1544,8 +1546,8 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
            S.nseg * S.gate_ctas * 2 <= 2 * kNumSms)
       S.gate_ctas *= 2;
     seg_tiles = std::min(seg_tiles, static_cast<long long>(S.ent_cap) * ((P.B + kt - 1) / kt));
-    const int rr = std::min(R, S.rows_per_tile);
-    S.gate_global = S.gate_ctas > 1 || static_cast<long long>(S.nb_cap) * (rr * 16 + 4) > kGateSmem;
+    S.gate_global = S.gate_ctas > 1 ||
+                    static_cast<long long>(S.nb_cap) * (S.gate_rows * 16 + 4) > kGateSmem;
   }
   // Few and short segments: a cluster has each to itself and joins it in its own memory, one launch
   // instead of two. Only while all clusters run at once, and while a warp then has little more to do
@@ -1569,7 +1571,7 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
 
 cudaError_t launch_paged_gate(const PagedLaunch& L, cudaStream_t s) {
   const PagedArgs A = args_of(L);
-  const int R = std::min(L.rows * A.group, L.shape.rows_per_tile);
+  const int R = L.shape.gate_rows;
 #define MOBA_GATE(D)                                     \
   return R <= 1   ? gate<D, 1>(A, L, s)                  \
          : R <= 2 ? gate<D, 2>(A, L, s)                  \

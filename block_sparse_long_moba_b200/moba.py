@@ -511,10 +511,9 @@ def _is(t, dtype, shape, device) -> bool:
             and t.is_contiguous())
 
 
-def _raw_stream(stream, device: torch.device) -> int:
-    """The cudaStream_t of `stream`, or of the device's current stream."""
-    return (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
-            else stream.cuda_stream)
+def _raw_stream(device: torch.device) -> int:
+    """The cudaStream_t of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _done(result, what: str):
@@ -541,13 +540,10 @@ def _rows(what: str, name: str, t: torch.Tensor, heads: Optional[int] = None,
     return s0 if T > 1 else h * w
 
 
-def _workspace(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace for one call. Memory of the caching allocator belongs to the current stream: a
-    call on another stream keeps it from being handed out before that stream is past the call."""
-    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    if stream is not None and stream != torch.cuda.current_stream():
-        ws.record_stream(stream)
-    return ws
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    """A workspace for one call. The calls below run on the current stream (one that is given is
+    made current first), so that what they allocate is memory of the stream that uses it."""
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -587,8 +583,12 @@ def moba_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
     """RMS norm of every head of q [T, Hq, d] and k [T, Hkv, d] (tokens may be strided) times fp32
     weights [d], and the rotary position of positions [T] in a table from rope_table. Returns
     packed (q_out, k_out)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moba_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps,
+                                     interleaved, q_out, k_out)
     what = "moba_qk_norm_rope"
-    if stream is None and _bind is not None:
+    if _bind is not None:
         done = _bind.norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved, q_out,
                                k_out)
         if done is not None:
@@ -605,7 +605,7 @@ def moba_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
     st = load_library().moba_qk_norm_rope(
         q.data_ptr(), q_ld, k.data_ptr(), k_ld, q_weight.data_ptr(), k_weight.data_ptr(),
         rope.data_ptr(), rope.shape[0], rope.shape[1], positions.data_ptr(), T, hq, hkv, d, eps,
-        1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), _raw_stream(stream, dev))
+        1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), _raw_stream(dev))
     _check(st, what)
     return q_out, k_out
 
@@ -620,8 +620,13 @@ def moba_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tens
                           workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients (dq, dk, d_q_weight, d_k_weight) of moba_qk_norm_rope; nothing but its inputs is
     needed from the forward pass."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moba_qk_norm_rope_bwd(q, k, q_weight, k_weight, rope, positions, d_q_out,
+                                         d_k_out, eps, interleaved, dq, dk, d_q_weight,
+                                         d_k_weight, workspace)
     what = "moba_qk_norm_rope_bwd"
-    if (stream is None and _bind is not None and dq is None and dk is None and d_q_weight is None
+    if (_bind is not None and dq is None and dk is None and d_q_weight is None
             and d_k_weight is None and workspace is None):
         done = _bind.norm_rope_bwd(q, k, q_weight, k_weight, rope, positions, d_q_out, d_k_out,
                                    eps, interleaved)
@@ -640,15 +645,14 @@ def moba_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tens
     _want(what, "d_k_weight", d_k_weight, torch.float32, (d,), dev)
     lib = load_library()
     if workspace is None:
-        workspace = _workspace(int(lib.moba_qk_norm_rope_bwd_workspace_bytes(hq, hkv, d)), dev,
-                               stream)
+        workspace = _workspace(int(lib.moba_qk_norm_rope_bwd_workspace_bytes(hq, hkv, d)), dev)
     _want(what, "workspace", workspace, torch.uint8, None, dev)
     st = lib.moba_qk_norm_rope_bwd(
         q.data_ptr(), q_ld, k.data_ptr(), k_ld, q_weight.data_ptr(), k_weight.data_ptr(),
         rope.data_ptr(), rope.shape[0], rope.shape[1], positions.data_ptr(), d_q_out.data_ptr(),
         d_k_out.data_ptr(), T, hq, hkv, d, eps, 1 if interleaved else 0, dq.data_ptr(),
         dk.data_ptr(), d_q_weight.data_ptr(), d_k_weight.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _raw_stream(stream, dev))
+        workspace.numel(), _raw_stream(dev))
     _check(st, what)
     return dq, dk, d_q_weight, d_k_weight
 
@@ -737,8 +741,11 @@ def moba_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor,
     """Writes the newest rows k, v [Tq, Hkv, d] bf16 (tokens may be strided) of every sequence
     (cu_seqlens_q [nseq + 1]; cache.seq_lens already counts them) into the cache's pages, rounded
     to 8 bits where the cache is e4m3, and adds the keys to their blocks' sums."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moba_cache_append(cache, k, v, cu_seqlens_q)
     what = "moba_cache_append"
-    if stream is None and _bind is not None and type(cache) is PagedCache:
+    if _bind is not None and type(cache) is PagedCache:
         done = _bind.append(cache._ref, cache._index, k, v, cu_seqlens_q)
         if done is not None:
             return _check(done, what)
@@ -753,7 +760,7 @@ def moba_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor,
         _want(what, "cu_seqlens_q", cu_seqlens_q, torch.int32, (cache.nseq + 1,), dev)
     _check(load_library().moba_cache_append(cache._ref, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
                                             cu_seqlens_q.data_ptr(), k.shape[0],
-                                            _raw_stream(stream, dev)), what)
+                                            _raw_stream(dev)), what)
 
 
 def moba_cache_read(cache: PagedCache, cu_seqlens: torch.Tensor, cu_seqlens_host,
@@ -761,11 +768,14 @@ def moba_cache_read(cache: PagedCache, cu_seqlens: torch.Tensor, cu_seqlens_host
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The first cu[s+1] - cu[s] cached tokens of every sequence, packed: (k, v) [T, Hkv, d] bf16
     as moba_attn_fwd takes them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moba_cache_read(cache, cu_seqlens, cu_seqlens_host, k, v)
     what = "moba_cache_read"
     dev = _cache(what, cache)._here(what)
     if len(cu_seqlens_host) != cache.nseq + 1:
         _bad(what, f"cu_seqlens_host must have {cache.nseq + 1} entries")
-    if stream is None and _bind is not None:
+    if _bind is not None:
         done = _bind.read(cache._ref, cache._index, cu_seqlens, int(cu_seqlens_host[-1]), k, v)
         if done is not None:
             return _done(done, what)
@@ -778,13 +788,13 @@ def moba_cache_read(cache: PagedCache, cu_seqlens: torch.Tensor, cu_seqlens_host
     _want(what, "k", k, torch.bfloat16, shape, dev)
     _want(what, "v", v, torch.bfloat16, shape, dev)
     _check(load_library().moba_cache_read(cache._ref, cu_seqlens.data_ptr(), shape[0],
-                                          k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev)), what)
+                                          k.data_ptr(), v.data_ptr(), _raw_stream(dev)), what)
     return k, v
 
 
-def _paged_plain(cache, q, rows_per_seq, topk, scale, idx, o, lse, workspace, stream):
+def _paged_plain(cache, q, rows_per_seq, topk, scale, idx, o, lse, workspace):
     """The call through csrc/bind.cpp, or None where its arguments are not plain."""
-    if (stream is not None or _bind is None or type(cache) is not PagedCache
+    if (_bind is None or type(cache) is not PagedCache
             or not torch.is_tensor(q) or q.dim() != 3):
         return None
     nbytes = 0 if workspace is not None else cache.workspace_bytes(q.shape[1], rows_per_seq, topk)
@@ -792,7 +802,7 @@ def _paged_plain(cache, q, rows_per_seq, topk, scale, idx, o, lse, workspace, st
                        workspace, nbytes)
 
 
-def _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace, stream):
+def _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace):
     """Checks and buffers that both attention calls over a paged cache share."""
     dev = _cache(what, cache)._here(what)
     if not torch.is_tensor(q) or q.dim() != 3:
@@ -812,7 +822,7 @@ def _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace, stream):
     else:
         _want(what, "lse", lse, torch.float32, (hq, n), dev)
     if workspace is None:
-        workspace = _workspace(cache.workspace_bytes(hq, rows_per_seq, topk), dev, stream)
+        workspace = _workspace(cache.workspace_bytes(hq, rows_per_seq, topk), dev)
     else:
         _want(what, "workspace", workspace, torch.uint8, None, dev)
     return dev, n, hq, o, lse, workspace
@@ -824,16 +834,19 @@ def moba_paged_attn_fwd(cache: PagedCache, q: torch.Tensor, rows_per_seq: int = 
                         workspace: Optional[torch.Tensor] = None, stream=None):
     """Full attention of the last rows_per_seq tokens of every cached sequence: q
     [nseq * rows_per_seq, Hq, d] bf16; returns (o like q, lse [Hq, rows] fp32)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moba_paged_attn_fwd(cache, q, rows_per_seq, scale, o, lse, workspace)
     what = "moba_paged_attn_fwd"
     if scale is None:
         scale = _cache(what, cache).d ** -0.5
-    done = _paged_plain(cache, q, rows_per_seq, 0, scale, None, o, lse, workspace, stream)
+    done = _paged_plain(cache, q, rows_per_seq, 0, scale, None, o, lse, workspace)
     if done is not None:
         return _done(done, what)
-    dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, 0, o, lse, workspace, stream)
+    dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, 0, o, lse, workspace)
     st = load_library().moba_paged_attn_fwd(
         cache._ref, q.data_ptr(), hq, rows_per_seq, scale, o.data_ptr(),
-        lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+        lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     _check(st, what)
     return o, lse
 
@@ -846,22 +859,25 @@ def moba_paged_decode_fwd(cache: PagedCache, q: torch.Tensor, topk: int, rows_pe
     """MoBA attention of the last rows_per_seq tokens of every cached sequence: routing by the
     cache's block_sums, then attention over the selected blocks. Returns (o, lse) as
     moba_paged_attn_fwd; block_idx_out [Hq, rows, topk] int32 receives the routing."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moba_paged_decode_fwd(cache, q, topk, rows_per_seq, scale, block_idx_out, o,
+                                         lse, workspace)
     what = "moba_paged_decode_fwd"
     if topk < 1 or not _cache(what, cache).block_size:
         _bad(what, "topk must be positive and the cache have block_sums")
     if scale is None:
         scale = cache.d ** -0.5
-    done = _paged_plain(cache, q, rows_per_seq, topk, scale, block_idx_out, o, lse, workspace,
-                        stream)
+    done = _paged_plain(cache, q, rows_per_seq, topk, scale, block_idx_out, o, lse, workspace)
     if done is not None:
         return _done(done, what)
-    dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace, stream)
+    dev, n, hq, o, lse, ws = _paged(what, cache, q, rows_per_seq, topk, o, lse, workspace)
     if block_idx_out is not None and not _is(block_idx_out, torch.int32, (hq, n, topk), dev):
         _want(what, "block_idx_out", block_idx_out, torch.int32, (hq, n, topk), dev)
     st = load_library().moba_paged_decode_fwd(
         cache._ref, q.data_ptr(), hq, rows_per_seq, topk, scale,
         None if block_idx_out is None else block_idx_out.data_ptr(), o.data_ptr(), lse.data_ptr(),
-        ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+        ws.data_ptr(), ws.numel(), _raw_stream(dev))
     _check(st, what)
     return o, lse
 

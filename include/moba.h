@@ -265,7 +265,9 @@ typedef struct {
  *   e4m3: a row of d keys (values) is stored as RN_e4m3(x / 2^e), 2^e the smallest power of two
  *   >= 2^-126 that keeps its largest magnitude within 448.
  *   block_sums (when given): blocks that begin with a new row are set to the sum of their new
- *   keys, a block that was begun before is added to. Column sums in a fixed order, fp32.
+ *   keys, a block that was begun before is added to. Column sums in a fixed order, fp32. A sequence
+ *   that is cut back into a block (rejected draft tokens) leaves their keys in that block's sum:
+ *   write the block again from its first row before its sum is used.
  * Rows whose page is outside the pool, whose position is negative or at or behind
  * max_pages * page_size, and rows at or behind cuq[nseq] are not written. No page may receive
  * rows of two sequences in one call.

@@ -304,6 +304,11 @@ DENSE = [  # lens, rows, hq, hkv, d, page, kv
     ([257, 600], 2, 33, 1, 64, 64, "e4m3"),           # 66 rows: five
     ([20000, 3], 1, 4, 1, 128, 256, "bf16"),          # one long sequence over many warps
     ([50, 60, 70] * 70, 1, 4, 2, 64, 16, "bf16"),     # more segments than warps share evenly
+    ([500, 7, 470, 512] * 4, 1, 32, 8, 128, 64, "e4m3"),  # a CTA per segment
+    ([500, 7, 470, 512] * 4, 1, 32, 8, 128, 32, "bf16"),
+    ([9000, 100], 4, 16, 2, 64, 64, "e4m3"),          # 32 rows a kv head over many warps
+    ([9000, 100], 4, 8, 2, 128, 64, "bf16"),          # 16 rows a kv head over many warps
+    ([17] * 900, 1, 2, 2, 64, 16, "e4m3"),            # many one-tile segments
 ]
 
 
@@ -343,6 +348,49 @@ def test_sharp_and_spread_out_logits(moba, kv):
     o, lse = moba.moba_paged_attn_fwd(S.cache, q, scale=0.3)
     want = cref.cached_attention(q, [x[0] for x in kv_rows], [x[1] for x in kv_rows], lens, 1, 0.3)
     _close(o, lse, want, _w(kv))
+
+
+def test_values_of_far_apart_scales(moba):
+    """e4m3: values 2^60 apart. A tiny weight on a huge value and a weight near one on small values
+    both count: o is the sum of the two, and a row that cannot see the huge value is exact without
+    it (the first of two rows)."""
+    n, d = 200, 64
+    S = Setup(moba, [n], 1, d, 16, "e4m3")
+    g = _gen(13)
+    k = torch.randn((n, 1, d), generator=g, device="cuda").bfloat16()
+    v = torch.randn((n, 1, d), generator=g, device="cuda").bfloat16()
+    v[n - 1] *= 2.0 ** 60
+    k[n - 1] = 0
+    k[n - 1, 0, 0] = -60.0
+    q = torch.randn((2, 1, d), generator=g, device="cuda").bfloat16()
+    q[:, 0, 0] = 1.0  # logit -60 in units of log e: a weight of about 2^-87 against 200 others
+    moba.moba_cache_append(S.cache, k, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    kk, vv = S.rows(0, n)
+    for scale in (0.5, 0.69, 1.0):
+        o, lse = moba.moba_paged_attn_fwd(S.cache, q, rows_per_seq=2, scale=scale)
+        want = cref.cached_attention(q, [kk], [vv], [n], 2, scale)
+        _close(o, lse, want, _w("e4m3"))
+
+
+def test_sequences_that_share_their_first_pages(moba):
+    """Two sequences with the same full pages for a common prefix, read by both at once."""
+    hkv, d, page, block, common = 2, 64, 16, 64, 128
+    S = Setup(moba, [200, 300], hkv, d, page, "bf16", block)
+    k, v = _fill(S, [200, 300])
+    shared = S.table.clone()
+    shared[0, :common // page] = shared[1, :common // page]
+    cache = moba.PagedCache(S.k, S.v, shared, S.lens, block_sums=S.sums, block_size=block)
+    S.table = shared
+    q = torch.randn((2, 4, d), generator=_gen(3), device="cuda").bfloat16()
+    rows = [S.rows(0, 200), S.rows(1, 300)]
+    assert np.array_equal(rows[0][0][:common], rows[1][0][:common])
+    sums = [cref.f64(S.sums[shared[s, :-(-x // page):4].long()]) for s, x in enumerate((200, 300))]
+    ks, vs = [x[0] for x in rows], [x[1] for x in rows]
+    o, lse = moba.moba_paged_attn_fwd(cache, q)
+    _close(o, lse, cref.cached_attention(q, ks, vs, [200, 300], 1, d ** -0.5), _w("bf16"))
+    o, lse = moba.moba_paged_decode_fwd(cache, q, 2)
+    _close(o, lse, cref.cached_attention(q, ks, vs, [200, 300], 1, d ** -0.5, sums, block, 2),
+           _w("bf16"))
 
 
 MOBA = [  # lens, rows, hq, hkv, d, page, block, topk, kv
@@ -513,6 +561,31 @@ def _near_tie(S, s, q, g, topk):
     order = np.argsort(-(sums @ q))
     a, b = sums[order[topk - 2]], sums[order[topk - 1]]
     assert a @ q - b @ q <= 2.0 ** -14 * max(np.abs(a) @ np.abs(q), np.abs(b) @ np.abs(q))
+
+
+def test_two_graphs_at_once(moba):
+    """Two captured steps with workspaces of their own, replayed on two streams at the same time."""
+    lens = [9000, 400]
+    S = Setup(moba, lens, 2, 128, 64, "e4m3", 128)
+    _fill(S, lens)
+    q = torch.randn((2, 2, 8, 128), generator=_gen(5), device="cuda").bfloat16()
+    call = lambda i: (moba.moba_paged_decode_fwd(S.cache, q[i], 6)  # noqa: E731
+                      + moba.moba_paged_attn_fwd(S.cache, q[i]))
+    want = [call(i) for i in range(2)]
+    graphs, outs = [], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(call(i))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
 
 
 def test_prefill_then_decode(moba):

@@ -52,6 +52,8 @@ CASES = [  # T, hq, hkv, d, rot, interleaved, fused
     (129, 7, 1, 128, 16, False, False),
     (64, 4, 2, 128, 96, True, True),
     (2000, 4, 1, 128, 48, False, False),
+    (20000, 32, 8, 128, 128, False, True),  # many chunks a warp
+    (7000, 20, 20, 64, 48, True, False),
 ]
 
 
