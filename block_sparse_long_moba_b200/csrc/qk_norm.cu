@@ -13,6 +13,9 @@
 // no exchange; products go two to an instruction; the sums of squares of a chunk's rows are reduced
 // together. Persistent: every warp takes a chunk of 2 KB (8 or 16 heads of one token) at a time
 // through a private ring in shared memory (16-byte cp.async, with the token's table row).
+// One CTA of 8 warps per SM and two rows at a time: fewer, longer streams suit HBM better than more
+// warps (128K tokens, 32 / 8 heads of 128, 2.7 GB: 407 us = 6.6 TB/s; two CTAs 467, three 465, four
+// rows at a time 440; gradients at 65521 tokens, 16 / 16 heads of 64: 127 us, two CTAs 138).
 #include <algorithm>
 #include <atomic>
 
@@ -31,7 +34,7 @@ constexpr int kChunkBytes = kIter * 512, kRopeBytes = 512;
 __host__ __device__ constexpr int stage_bytes(bool bwd) {
   return (bwd ? 2 : 1) * kChunkBytes + kRopeBytes;
 }
-constexpr int norm_stages(bool bwd) { return bwd ? 3 : 5; }
+constexpr int norm_stages(bool bwd) { return bwd ? 3 : 4; }
 constexpr int norm_smem(bool bwd) { return kNormWarps * norm_stages(bwd) * stage_bytes(bwd); }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
@@ -212,7 +215,7 @@ __host__ __device__ constexpr int chunk_rows(int d) { return kChunkBytes / (2 * 
 // Forward: y_a = r (x_a (w_a c) - x_b (w_b s)), y_b = r (x_b (w_b c) + x_a (w_a s)), the weights
 // multiplied into the token's angle once for all rows of the chunk. Backward: as stated at the top.
 template <int D, bool ADJ, bool BWD>
-__global__ void __launch_bounds__(kNormThreads, 2) qk_norm_rope_kernel(const NormArgs A) {
+__global__ void __launch_bounds__(kNormThreads, 1) qk_norm_rope_kernel(const NormArgs A) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, kStage = stage_bytes(BWD);
   constexpr int kStages = norm_stages(BWD);
   extern __shared__ __align__(128) uint8_t smem[];
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_rope_kernel(const Nor
           ws.b[e] = mul2(neg2(w.b[e]), R.s[e]);
         }
       s += sub * 2 * D;
-      constexpr int NB = BWD ? 2 : kIter, N = 4;  // rows and sums of a batch (registers)
+      constexpr int NB = 2, N = BWD ? 4 : 2;  // rows and sums of a batch
 #pragma unroll
       for (int i0 = 0; i0 < kIter; i0 += NB) {
         // the rows' sums first, all together, so that their shuffles overlap
@@ -422,11 +425,10 @@ NormArgs args_of(const NormLaunch& L) {
   return A;
 }
 
-// CTAs: what fits the SMs at once (two of 8 warps, their rings 100 or 108 KB), at least a warp
-// for every chunk of a token, and no more than there are units.
+// CTAs: one per SM, at least a warp for every chunk of a token, and no more than there are units.
 int norm_ctas(int chunks, long long T) {
   const long long all = (T * chunks + kNormWarps - 1) / kNormWarps;
-  const long long most = 2ll * kNumSms;
+  const long long most = kNumSms;
   return static_cast<int>(std::max<long long>(std::min(all, most),
                                               (chunks + kNormWarps - 1) / kNormWarps));
 }
