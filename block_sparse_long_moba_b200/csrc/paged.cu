@@ -17,7 +17,9 @@
 // the 128-row tile of tcgen05.mma would be 1/8 full at best; here a row tile of 8 wastes at most
 // 7 rows, and the tensor pipe stays far below the memory time: 16 cached bf16 rows of K and V at
 // d = 128 are 8 KB = ~350 clocks of one SM's share of HBM against 16 mma of 16 clocks on each of
-// four tensor units. Bound: HBM, each selected key and value row once.
+// four tensor units. Bound: HBM, each selected key and value row once. Measured, 32 / 8 heads of
+// 128: 8 x 128K tokens of which the heads of a kv group select 26 of 32 blocks of 4096, 3.6 GB, 535 us
+// (6.7 TB/s); a ragged batch of 32 with 0.69 GB, 110 us (6.2 TB/s); 1000 tokens, 9 us (latency).
 //
 // e4m3 caches: codes widen exactly to f16, products run in f16 with fp32 accumulation. q is bf16
 // and becomes f16 exactly after a power-of-two scaling of its row (elements 2^-25 below the row's
@@ -47,8 +49,8 @@ namespace {
 
 // Warps of a CTA and bytes of K (and of V) per stage: 192 KB of ring either way. An e4m3 tile takes
 // about 930 instructions per 64 keys, a third of them widening codes, so one warp per scheduler
-// cannot keep up with HBM on its dependent steps; two with half the tile can (8 x 128K tokens:
-// measured 365 us with 4 warps and 8 KB, see the figures at the kernel).
+// cannot keep up with HBM on its dependent steps; two with half the tile can (8 x 128K tokens, 32 / 8
+// heads of 128: 330 us, 6.5 TB/s; 365 us with 4 warps and 8 KB).
 __host__ __device__ constexpr int paged_warps(bool fp8) { return fp8 ? 8 : 4; }
 __host__ __device__ constexpr int tile_bytes(bool fp8) { return fp8 ? 4096 : 8192; }
 constexpr int kStages = 3;
@@ -244,66 +246,66 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
     ub = me < workers ? range_start(U, me, workers) : 0;
     ue = me < workers ? range_start(U, me + 1, workers) : 0;
   } else {
-  // Prefix sums: thread t owns a run of segments.
-  const int per = (A.nseg + kPagedThreads - 1) / kPagedThreads;
-  {
-    long long mine = 0;
-    const int a = min(A.nseg, tid * per), b = min(A.nseg, a + per);
-    for (int i = a; i < b; ++i) mine += tiles_of(i);
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) prefix[warp] = incl;
-    __syncthreads();
-    long long before = 0, all = 0;
-    for (int w = 0; w < kPagedWarps; ++w) {
-      const long long x = prefix[w];
-      if (w < warp) before += x;
-      all += x;
-    }
-    __syncthreads();
-    prefix[tid] = before + incl - mine;
-    if (tid == 0) prefix[kPagedThreads] = all;
-    __syncthreads();
-  }
-  U = prefix[kPagedThreads];
-  // Neighbouring workers sit on different SMs, so that few tiles still use many of them.
-  workers = static_cast<int>(min(static_cast<long long>(gridDim.x) * kPagedWarps, U));
-  me = warp * gridDim.x + blockIdx.x;
-  if (me >= workers) return;  // no block-wide barrier below on this path
-  ub = range_start(U, me, workers);
-  ue = range_start(U, me + 1, workers);
-
-  // Segment of tile ub: the run that holds it, then 32 segments at a time.
-  {
-    int run = 0;
-    for (int x = lane; x < kPagedThreads; x += 32)
-      if (prefix[x] <= ub) run = x;  // ascending in x per lane
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) run = max(run, __shfl_xor_sync(0xffffffffu, run, o));
-    long long at = prefix[run];
-    const int last = min(A.nseg, (run + 1) * per);
-    for (int i = run * per; i < last; i += 32) {
-      const int cnt = i + lane < last ? tiles_of(i + lane) : 0;
-      long long incl = cnt;
+    // Prefix sums: thread t owns a run of segments.
+    const int per = (A.nseg + kPagedThreads - 1) / kPagedThreads;
+    {
+      long long mine = 0;
+      const int a = min(A.nseg, tid * per), b = min(A.nseg, a + per);
+      for (int i = a; i < b; ++i) mine += tiles_of(i);
+      long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, at + incl > ub);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        seg0 = i + src;
-        seg_begin = at + __shfl_sync(0xffffffffu, incl - cnt, src);
-        break;
+      if (lane == 31) prefix[warp] = incl;
+      __syncthreads();
+      long long before = 0, all = 0;
+      for (int w = 0; w < kPagedWarps; ++w) {
+        const long long x = prefix[w];
+        if (w < warp) before += x;
+        all += x;
       }
-      at += __shfl_sync(0xffffffffu, incl, 31);
+      __syncthreads();
+      prefix[tid] = before + incl - mine;
+      if (tid == 0) prefix[kPagedThreads] = all;
+      __syncthreads();
     }
-  }
+    U = prefix[kPagedThreads];
+    // Neighbouring workers sit on different SMs, so that few tiles still use many of them.
+    workers = static_cast<int>(min(static_cast<long long>(gridDim.x) * kPagedWarps, U));
+    me = warp * gridDim.x + blockIdx.x;
+    if (me >= workers) return;  // no block-wide barrier below on this path
+    ub = range_start(U, me, workers);
+    ue = range_start(U, me + 1, workers);
+
+    // Segment of tile ub: the run that holds it, then 32 segments at a time.
+    {
+      int run = 0;
+      for (int x = lane; x < kPagedThreads; x += 32)
+        if (prefix[x] <= ub) run = x;  // ascending in x per lane
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) run = max(run, __shfl_xor_sync(0xffffffffu, run, o));
+      long long at = prefix[run];
+      const int last = min(A.nseg, (run + 1) * per);
+      for (int i = run * per; i < last; i += 32) {
+        const int cnt = i + lane < last ? tiles_of(i + lane) : 0;
+        long long incl = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, at + incl > ub);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          seg0 = i + src;
+          seg_begin = at + __shfl_sync(0xffffffffu, incl - cnt, src);
+          break;
+        }
+        at += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
   }
 
   uint8_t* wbase = smem + warp * TL::kWarpBytes;
@@ -1000,9 +1002,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
 // the page ids and q are fetched before the sequence's length is known; all rows' partial sums of
 // a block are reduced together, a lane keeping half of its values at each step; and the selection is
 // ranking by 32 shuffles (at most 32 past blocks), one warp per row with its keys in registers (at
-// most 256), or one CTA per row (beyond; keys in registers up to 2048). The latter two are a radix selection on
-// order-preserving 64-bit keys whose 256 bins span only the range still in question: usually two
-// or three sweeps instead of the eight that fixed bytes of an fp64 key would take.
+// most 256), or one CTA per row (beyond; keys in registers up to 2048). The latter two are a radix
+// selection on order-preserving 64-bit keys whose 256 bins span only the range still in question:
+// usually two sweeps instead of the eight that fixed bytes of an fp64 key would take.
+// Measured inside the kernel, in clocks: 31 past blocks and 4 rows, 10,000 (lengths and q 2,600,
+// scores 3,000, selection 2,300, list 2,200; a step runs once, so much of it is the first fetch of
+// its instructions); 1791 blocks of d = 64 and one row over 4 CTAs, 20,000.
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
 constexpr int kGateInRegs = 8;  // keys a thread holds in a selection
@@ -1040,7 +1045,8 @@ __device__ __forceinline__ void reduce_rows8(double (&v)[RR], int lane) {
 }
 
 // One bin of a radix pass: the highest bin that brings the count from the top to `want`.
-// Returns the bin, the keys in it and the keys above it; every lane of the warp gets them.
+// Returns the bin, the keys in it (0 when the bins hold fewer than `want`) and the keys above it;
+// every lane of the warp gets them.
 __device__ __forceinline__ void pick_bin(const int* hist, int want, int lane, int* bin, int* cnt,
                                          int* above) {
   int bins[8], mine = 0;  // lane 0 has the eight highest bins
@@ -1063,9 +1069,9 @@ __device__ __forceinline__ void pick_bin(const int* hist, int want, int lane, in
       if (ab + bins[x] >= want) { b = 255 - (lane * 8 + x); c = bins[x]; }
       else ab += bins[x];
     }
-  *bin = __shfl_sync(0xffffffffu, b, src);
-  *cnt = __shfl_sync(0xffffffffu, c, src);
-  *above = __shfl_sync(0xffffffffu, ab, src);
+  *bin = __shfl_sync(0xffffffffu, b, src & 31);
+  *cnt = src < 0 ? 0 : __shfl_sync(0xffffffffu, c, src & 31);
+  *above = __shfl_sync(0xffffffffu, ab, src & 31);
 }
 
 // State of a radix selection of the `want` largest keys: keys above thr are in, and the first
@@ -1075,6 +1081,21 @@ struct Radix {
   int want, need_eq;
   __device__ __forceinline__ int shift() const {
     return max(0, 56 - __clzll(static_cast<long long>(range)));
+  }
+  __device__ __forceinline__ void all(unsigned long long lo, unsigned long long hi) {
+    thr = lo;
+    range = hi - lo;
+  }
+  // The search begins in the four binades below a positive largest score, where the largest keys
+  // nearly always are: bins over all keys would be as wide as sixteen binades and put most of the
+  // keys into a few of them. all() starts again where that range holds too few.
+  __device__ __forceinline__ void start(unsigned long long lo, unsigned long long hi) {
+    all(lo, hi);
+    if (hi > 0x8000000000000000ull) {
+      const double top = __longlong_as_double(static_cast<long long>(hi ^ 0x8000000000000000ull));
+      const unsigned long long from = order_key64(top * 0.0625);
+      if (from > lo && from < hi) all(from, hi);
+    }
   }
   // Narrows to the picked bin; true when the selection is settled.
   __device__ __forceinline__ bool narrow(int bin, int cnt, int above) {
@@ -1115,6 +1136,8 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
   const int R = A.rows * A.group, row0 = id.rt * kRows;
   const int nrow = min(kRows, R - row0);  // rows of this tile (<= RR)
   const int32_t* pages = A.page_table + static_cast<size_t>(id.s) * A.max_pages;
+  bool over;
+  const int L = seq_len(A, id.s, &over);
   // eight lanes per block: this group's blocks are first, first + stride, ...
   const int first = (rank * kGateWarps + warp) * 4 + (lane >> 3), stride = CS * kGateWarps * 4;
   auto page_of = [&](int j) {
@@ -1132,8 +1155,6 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
     for (int x = lane; x < D; x += 32)
       qd[r][x] = r < nrow ? static_cast<double>(__bfloat162float(src[x])) : 0.;
   }
-  bool over;
-  const int L = seq_len(A, id.s, &over);
   const int last = L > 0 ? (L - 1) / A.B : -1;  // current block of the newest row
   unsigned long long* keys =
       in_smem ? skeys : A.keys + static_cast<size_t>(seg) * min(kRows, R) * A.nb_cap;
@@ -1161,38 +1182,43 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) pid[u] = page_of(j0 + (U + u) * stride);
+      // all of the round's chains side by side (an fp64 step takes tens of clocks); blocks behind
+      // the last are computed and dropped
+      double v[U][RR];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < RR; ++r) v[u][r] = 0.;
+#pragma unroll
+      for (int x = 0; x < NV; ++x)
+#pragma unroll
+        for (int r = 0; r < RR; ++r) {
+          const double2* qp = reinterpret_cast<const double2*>(&qd[r][(l8 + 8 * x) * 4]);
+          const double2 a = qp[0], b = qp[1];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            v[u][r] = fma(a.x, static_cast<double>(c[u][x].x), v[u][r]);
+            v[u][r] = fma(a.y, static_cast<double>(c[u][x].y), v[u][r]);
+            v[u][r] = fma(b.x, static_cast<double>(c[u][x].z), v[u][r]);
+            v[u][r] = fma(b.y, static_cast<double>(c[u][x].w), v[u][r]);
+          }
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) reduce_rows8<RR>(v[u], lane);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = j0 + u * stride;
-        if (j - (lane >> 3) >= last) break;  // uniform over the warp
-        double v[RR];
-#pragma unroll
-        for (int r = 0; r < RR; ++r) v[r] = 0.;
-#pragma unroll
-        for (int x = 0; x < NV; ++x) {
-          const double cd[4] = {c[u][x].x, c[u][x].y, c[u][x].z, c[u][x].w};
-#pragma unroll
-          for (int r = 0; r < RR; ++r) {
-            const double2* qp = reinterpret_cast<const double2*>(&qd[r][(l8 + 8 * x) * 4]);
-            const double2 a = qp[0], b = qp[1];
-            v[r] = fma(a.x, cd[0], v[r]);
-            v[r] = fma(a.y, cd[1], v[r]);
-            v[r] = fma(b.x, cd[2], v[r]);
-            v[r] = fma(b.y, cd[3], v[r]);
-          }
-        }
-        reduce_rows8<RR>(v, lane);
         if (j < last) {
           if constexpr (RR >= 8) {
 #pragma unroll
             for (int i = 0; i < RR / 8; ++i) {
               const int r = l8 * (RR / 8) + i;
-              if (r < nrow) keys[static_cast<size_t>(r) * A.nb_cap + j] = order_key64(v[i]);
+              if (r < nrow) keys[static_cast<size_t>(r) * A.nb_cap + j] = order_key64(v[u][i]);
             }
           } else {
             const int r = l8 / (8 / RR);
             if (l8 % (8 / RR) == 0 && r < nrow)
-              keys[static_cast<size_t>(r) * A.nb_cap + j] = order_key64(v[0]);
+              keys[static_cast<size_t>(r) * A.nb_cap + j] = order_key64(v[u][0]);
           }
         }
       }
@@ -1215,63 +1241,76 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
     if (RR > 1) atomicOr(marks + j, 1u << r);
     else ent[at] = make_int2(j, 1);
   };
-  if (last <= 32 * kGateInRegs) {
+  if (last <= 32) {
+    // row r by warp r / CS of rank r % CS, a block per lane, ranked by its score. (Its own code, as
+    // short as it gets: at one pass through it, fetching instructions is what takes the time.)
+    for (int r = rank + CS * warp; r < nrow; r += CS * kGateWarps) {
+      int i;
+      int32_t* out = place(r, &i);
+      const int want = min(A.topk - 1, max(i, 0));
+      int before = 0;  // blocks selected before this lane's
+      if (want > 0 && want < i) {
+        const unsigned long long k =
+            lane < i ? keys[static_cast<size_t>(r) * A.nb_cap + lane] : 0ull;
+#pragma unroll 4
+        for (int x = 0; x < i; ++x) {
+          const unsigned long long other = __shfl_sync(0xffffffffu, k, x);
+          before += other > k || (other == k && x < lane);
+        }
+      }
+      const bool sel = lane < i && before < want;
+      const unsigned sels = __ballot_sync(0xffffffffu, sel);
+      if (sel) take(out, r, __popc(sels & ((1u << lane) - 1)), lane);
+      if (i >= 0 && lane == 0) take(out, r, want, i);
+      if (out)
+        for (int x = (i >= 0 ? want + 1 : 0) + lane; x < A.topk; x += 32) out[x] = -1;
+      if (RR == 1 && lane == 0) stot = i >= 0 ? want + 1 : 0;
+    }
+  } else if (last <= 32 * kGateInRegs) {
     // row r by warp r / CS of rank r % CS
     for (int r = rank + CS * warp; r < nrow; r += CS * kGateWarps) {
       int i;
       int32_t* out = place(r, &i);
       const int want = min(A.topk - 1, max(i, 0));
       unsigned long long kk[kGateInRegs];
-      Radix S{0ull, 0ull, want, 0x7fffffff};
-      bool ranked = false, in32 = false;
+      Radix S{0ull, 0ull, want, want};
       if (want > 0 && want < i) {
         const unsigned long long* kr = keys + static_cast<size_t>(r) * A.nb_cap;
 #pragma unroll
         for (int x = 0; x < kGateInRegs; ++x)
           kk[x] = x * 32 + lane < i ? kr[x * 32 + lane] : 0ull;
-        if (i <= 32) {
-          int rank32 = 0;  // keys before this lane's in the order of selection
-          for (int x = 0; x < i; ++x) {
-            const unsigned long long k = __shfl_sync(0xffffffffu, kk[0], x);
-            rank32 += k > kk[0] || (k == kk[0] && x < lane);
+        unsigned long long lo = ~0ull, hi = 0;
+#pragma unroll
+        for (int x = 0; x < kGateInRegs; ++x)
+          if (x * 32 + lane < i) {
+            lo = min(lo, kk[x]);
+            hi = max(hi, kk[x]);
           }
-          ranked = true;
-          in32 = rank32 < want;
-        } else {
-          unsigned long long lo = ~0ull, hi = 0;
 #pragma unroll
-          for (int x = 0; x < kGateInRegs; ++x)
-            if (x * 32 + lane < i) {
-              lo = min(lo, kk[x]);
-              hi = max(hi, kk[x]);
-            }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-          }
-          S.thr = lo;
-          S.range = hi - lo;
-          S.need_eq = want;
-          if (S.range)
-            while (true) {
-              const int sh = S.shift();
-#pragma unroll
-              for (int x = 0; x < 8; ++x) hist[warp][x * 32 + lane] = 0;
-              __syncwarp();
-#pragma unroll
-              for (int x = 0; x < kGateInRegs; ++x) {
-                const unsigned long long d = kk[x] - S.thr;  // wraps above range for lower keys
-                if (x * 32 + lane < i && d <= S.range)
-                  atomicAdd(&hist[warp][static_cast<int>(d >> sh)], 1);
-              }
-              __syncwarp();
-              int bin, cnt, above;
-              pick_bin(hist[warp], S.want, lane, &bin, &cnt, &above);
-              if (S.narrow(bin, cnt, above)) break;
-              __syncwarp();
-            }
+        for (int o = 16; o > 0; o >>= 1) {
+          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
+        S.start(lo, hi);
+        if (S.range)
+          while (true) {
+            const int sh = S.shift();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) hist[warp][x * 32 + lane] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < kGateInRegs; ++x) {
+              const unsigned long long d = kk[x] - S.thr;  // wraps above range for lower keys
+              if (x * 32 + lane < i && d <= S.range)
+                atomicAdd(&hist[warp][static_cast<int>(d >> sh)], 1);
+            }
+            __syncwarp();
+            int bin, cnt, above;
+            pick_bin(hist[warp], S.want, lane, &bin, &cnt, &above);
+            if (cnt == 0) S.all(lo, hi);
+            else if (S.narrow(bin, cnt, above)) break;
+            __syncwarp();
+          }
       }
       int at = 0, eq = 0;
       if (want > 0) {
@@ -1279,8 +1318,8 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
         for (int x = 0; x < kGateInRegs; ++x) {
           const int j = x * 32 + lane;
           if (x * 32 >= i) break;
-          bool sel = j < i && (want == i || (ranked ? in32 : kk[x] > S.thr));
-          if (want < i && !ranked) {
+          bool sel = j < i && (want == i || kk[x] > S.thr);
+          if (want < i) {
             const bool same = j < i && kk[x] == S.thr;
             const unsigned eqs = __ballot_sync(0xffffffffu, same);
             if (same) sel = eq + __popc(eqs & ((1u << lane) - 1)) < S.need_eq;
@@ -1341,7 +1380,8 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
           lo = min(lo, slo[w]);
           hi = max(hi, shi[w]);
         }
-        Radix S{lo, hi - lo, want, want};
+        Radix S{0ull, 0ull, want, want};
+        S.start(lo, hi);
         if (S.range)
           while (true) {
             const int sh = S.shift();
@@ -1353,7 +1393,8 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
             int bin, cnt, above;
             pick_bin(hist[0], S.want, lane, &bin, &cnt, &above);  // every warp alike
             __syncthreads();
-            if (S.narrow(bin, cnt, above)) break;
+            if (cnt == 0) S.all(lo, hi);
+            else if (S.narrow(bin, cnt, above)) break;
             hist[0][tid] = 0;
             __syncthreads();
           }
@@ -1409,12 +1450,21 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
   if (RR > 1) sync_all();      // all rows' marks
   else __syncthreads();        // stot (rank 0 has the one row)
   if (rank == 0) {  // the blocks that a row selected, ascending
-    bool bad = over;
-    for (int r = 0; r < CS; ++r) bad |= *cluster.map_shared_rank(&sbad, r) != 0;
+    const int few = last < 32 * kGateInRegs;  // one warp lists them, without barriers
     int total = 0, has_last = 0;
     if (RR == 1) {
       total = last >= 0 ? stot : 0;
       has_last = total > 0;  // the one row is the newest
+    } else if (few) {
+      if (warp > 0) total = -1;  // not this warp's
+      for (int j0 = 0; j0 <= last && warp == 0; j0 += 32) {
+        const unsigned int mk = j0 + lane <= last ? marks[j0 + lane] : 0u;
+        const unsigned b = __ballot_sync(0xffffffffu, mk != 0);
+        if (mk)
+          ent[total + __popc(b & ((1u << lane) - 1))] = make_int2(j0 + lane, static_cast<int>(mk));
+        total += __popc(b);
+        if (last < j0 + 32) has_last = (b >> (last - j0)) & 1;
+      }
     } else {
       for (int j0 = 0; j0 <= last; j0 += kGateThreads) {
         const int j = j0 + tid;
@@ -1432,9 +1482,11 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
         if (mk) ent[before + __popc(b & ((1u << lane) - 1))] = make_int2(j, static_cast<int>(mk));
         __syncthreads();
       }
-      if (last >= 0) has_last = stot;
+      has_last = stot;
     }
     if (tid == 0) {
+      bool bad = over || sbad != 0;
+      for (int r = 1; r < CS; ++r) bad |= *cluster.map_shared_rank(&sbad, r) != 0;
       const int tail = L - max(last, 0) * A.B;
       A.seg_tiles[seg] = bad ? -1
                              : (total - has_last) * A.tiles_per_block +
