@@ -827,7 +827,7 @@ int moba_qk_norm_rope(const void* q, long long q_stride, const void* k, long lon
 
 size_t moba_qk_norm_rope_bwd_workspace_bytes(int Hq, int Hkv, int d) {
   if (Hq < 1 || Hkv < 1 || Hq > 65536 || Hkv > 65536 || (d != 64 && d != 128)) return 0;
-  return up256(static_cast<size_t>(qk_norm_bwd_ctas(Hq, Hkv, d, 0x7fffffff)) * 2 * d * 4);
+  return up256(static_cast<size_t>(qk_norm_bwd_max_parts(Hq, Hkv, d)) * 2 * d * 4);
 }
 
 int moba_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long long k_stride,
@@ -854,12 +854,12 @@ int moba_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long
   N.dyq = d_q_out; N.dyk = d_k_out; N.oq = dq; N.ok = dk;
   N.part = static_cast<float*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // no rows: the weights' gradients are zero (a sum over no CTA)
-  const int ctas = T > 0 ? qk_norm_bwd_ctas(Hq, Hkv, d, T) : 0;
+  // no rows: the weights' gradients are zero (a sum over no part)
+  const int parts = T > 0 ? qk_norm_bwd_parts(Hq, Hkv, d, T) : 0;
   if (T > 0)
-    MOBA_LAUNCH_NAMED(-1, "moba_qk_norm_rope_bwd", s, launch_qk_norm_bwd(N, ctas, s));
+    MOBA_LAUNCH_NAMED(-1, "moba_qk_norm_rope_bwd", s, launch_qk_norm_bwd(N, s));
   MOBA_LAUNCH_NAMED(-1, "moba_qk_norm_dw", s,
-                    launch_qk_norm_dw(N.part, ctas, d, d_q_weight, d_k_weight, s));
+                    launch_qk_norm_dw(N.part, parts, d, d_q_weight, d_k_weight, s));
   return MOBA_OK;
 }
 

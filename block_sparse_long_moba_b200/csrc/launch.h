@@ -212,8 +212,9 @@ struct NormLaunch {
   float eps;
 };
 cudaError_t launch_qk_norm(const NormLaunch& L, cudaStream_t s);
-int qk_norm_bwd_ctas(int Hq, int Hkv, int d, int T);  // at most that of T = INT_MAX
-cudaError_t launch_qk_norm_bwd(const NormLaunch& L, int ctas, cudaStream_t s);
+int qk_norm_bwd_parts(int Hq, int Hkv, int d, int T);     // partial sums of the weights' gradients
+int qk_norm_bwd_max_parts(int Hq, int Hkv, int d);        // at most, for any T
+cudaError_t launch_qk_norm_bwd(const NormLaunch& L, cudaStream_t s);
 cudaError_t launch_qk_norm_dw(const float* part, int n, int d, float* dwq, float* dwk,
                               cudaStream_t s);
 

@@ -1595,7 +1595,7 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
     // A CTA scores 32 blocks at a time. More CTAs per segment while they all run at once (two fit
     // an SM); keys and marks of a single CTA stay in its shared memory where they fit.
     while (S.gate_ctas < 8 && S.nb_cap > 64 * S.gate_ctas &&
-           S.nseg * S.gate_ctas * 2 <= 2 * kNumSms)
+           S.nseg * S.gate_ctas * 2 <= 256)  // 32 clusters of 8, 64 of 4
       S.gate_ctas *= 2;
     seg_tiles = std::min(seg_tiles, static_cast<long long>(S.ent_cap) * ((P.B + kt - 1) / kt));
     S.gate_global = S.gate_ctas > 1 ||
@@ -1608,11 +1608,15 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
   // clusters at most two. Measured, d = 128, 32 / 8 heads, joined against spread and merged:
   // 16 x 500 tokens 10 us : 15 (either type), 1 x 4000 bf16 11.8 : 13.0, 1 x 8000 bf16 (4.4 tiles
   // more per warp) 15.2 : 15.0, 4 x 1000 e4m3 (1.1 more) 12.4 : 11.8.
+  // At once means 16 clusters of 8, 32 of 4 or 72 of 2 (a cluster lies within one of the GPU's
+  // groups of 18 or 20 SMs): 18 clusters of 8 took 27 us where 9 take 14.
   if (S.nseg <= sms) {
     const int most = P.fp8 ? 2 : 8;
     const double margin = P.fp8 ? 0.75 : 3.0;
+    auto at_once = [](int c) { return c == 2 ? 72 : c == 4 ? 32 : 16; };
     int cs = 1;
-    while (cs < most && S.nseg * cs * 2 <= sms && seg_tiles > static_cast<long long>(cs) * warps)
+    while (cs < most && S.nseg <= at_once(2 * cs) &&
+           seg_tiles > static_cast<long long>(cs) * warps)
       cs *= 2;
     const double joined = static_cast<double>(seg_tiles) / (cs * warps);
     const double spread = static_cast<double>(seg_tiles) * S.nseg / (sms * warps);

@@ -386,6 +386,188 @@ __global__ void __launch_bounds__(kNormThreads, 1) qk_norm_rope_kernel(const Nor
   }
 }
 
+// The same for ONE of q and k with fewer heads than a chunk has rows: a chunk is then consecutive
+// (token, head) rows across tokens, so that it stays full, and every row has an angle of its own.
+// Those come straight from the table into registers one unit ahead (their positions two ahead).
+struct RowsArgs {
+  const __nv_bfloat16 *x, *dy;
+  long long ld;
+  const float *w, *rope;
+  const int32_t* pos;
+  __nv_bfloat16* out;
+  float* part;          // backward: [CTAs][2][D]
+  int rows, H, n_pos, rot;
+  uint32_t magic;       // row / H = umulhi(row, magic) >> shift for rows < 2^31, H > 1
+  int shift, which;     // which: 0 for q, 1 for k
+  float eps;
+};
+
+template <int D, bool ADJ, bool BWD>
+__global__ void __launch_bounds__(kNormThreads, BWD ? 1 : 2) norm_rope_rows_kernel(const RowsArgs A) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, kRows = chunk_rows(D);
+  constexpr int kStage = (BWD ? 2 : 1) * kChunkBytes, kStages = BWD ? 4 : 6;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[BWD ? kNormWarps : 1][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
+  const int G = static_cast<int>(gridDim.x) * kNormWarps;
+  const int g = static_cast<int>(blockIdx.x) * kNormWarps + warp;
+  const Place<ADJ> P(l, A.rot);
+  const bool all = A.rot == D;
+  wait_previous_kernel();
+  Elems acc;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) acc.a[e] = acc.b[e] = make_float2(0.f, 0.f);
+  const int chunks = (A.rows + kRows - 1) / kRows;
+  const int units = g < chunks ? (chunks - g + G - 1) / G : 0;
+  if (units > 0) {
+    const Elems w = read_weights<ADJ>(A.w, P);
+    uint8_t* ring = smem + warp * (kStages * kStage);
+    const uint32_t lane_dst = smem_u32(ring) + lane * 16;
+    // row of piece i of unit n, below 2^31 + a grid's worth; its token
+    auto row_of = [&](int n, int i) {
+      return (static_cast<uint32_t>(g) + static_cast<uint32_t>(n) * G) * kRows + i * RPW + sub;
+    };
+    auto token_of = [&](uint32_t r) {
+      return A.H == 1 ? r : __umulhi(r, A.magic) >> A.shift;
+    };
+    auto issue = [&](int n, int stage) {
+      if (n < units) {
+        const uint32_t d = lane_dst + stage * kStage;
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const uint32_t r = row_of(n, i);
+          const bool in = r < static_cast<uint32_t>(A.rows);
+          const uint32_t t = token_of(in ? r : 0);
+          const long long at = t * A.ld + static_cast<long long>((in ? r : 0) - t * A.H) * D;
+          copy16(d + i * 512, A.x + at + l * 8, in);
+          if (BWD)
+            copy16(d + kChunkBytes + i * 512, A.dy + static_cast<size_t>(in ? r : 0) * D + l * 8,
+                   in);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto fetch_pos = [&](int n, int (&p)[kIter]) {
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const uint32_t r = row_of(n, i);
+        p[i] = n < units && r < static_cast<uint32_t>(A.rows) ? __ldg(A.pos + token_of(r)) : -1;
+      }
+    };
+    auto fetch_angles = [&](const int (&p)[kIter], Angle (&R)[kIter]) {
+#pragma unroll
+      for (int i = 0; i < kIter; ++i)
+        R[i] = read_angle(
+            A.rope + static_cast<size_t>(p[i] >= 0 && p[i] < A.n_pos ? p[i] : 0) * A.rot, l, A.rot,
+            all);
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+    int p0[kIter], p1[kIter];  // positions of the unit in work and of the next
+    Angle R1[kIter];           // angles of the next
+    fetch_pos(0, p1);
+    fetch_angles(p1, R1);
+    int p2[kIter];
+    fetch_pos(1, p2);
+    int stage = 0;
+    for (int n = 0; n < units; ++n) {
+      Angle R[kIter];
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        R[i] = R1[i];
+        p0[i] = p1[i];
+        p1[i] = p2[i];
+      }
+      if (n + 1 < units) fetch_angles(p1, R1);
+      fetch_pos(n + 2, p2);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();
+      issue(n + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+      const uint8_t* s = ring + stage * kStage + sub * 2 * D;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      constexpr int NB = 2, N = BWD ? 4 : 2;
+#pragma unroll
+      for (int i0 = 0; i0 < kIter; i0 += NB) {
+        Elems x[NB], z[BWD ? NB : 1];
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          x[i] = read_row<ADJ>(s + (i0 + i) * 512, P);
+          float2 sq = mul2(x[i].a[0], x[i].a[0]);
+          sq = fma2(x[i].a[1], x[i].a[1], sq);
+          sq = fma2(x[i].b[0], x[i].b[0], sq);
+          sq = fma2(x[i].b[1], x[i].b[1], sq);
+          v[i] = sq.x + sq.y;
+          if constexpr (BWD) {
+            const Elems y = read_row<ADJ>(s + kChunkBytes + (i0 + i) * 512, P);
+            float2 dt = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              z[i].a[e] = fma2(y.a[e], R[i0 + i].c[e], mul2(y.b[e], R[i0 + i].s[e]));
+              z[i].b[e] = fma2(y.b[e], R[i0 + i].c[e], mul2(neg2(y.a[e]), R[i0 + i].s[e]));
+              dt = fma2(mul2(z[i].a[e], w.a[e]), x[i].a[e], dt);
+              dt = fma2(mul2(z[i].b[e], w.b[e]), x[i].b[e], dt);
+            }
+            v[NB + i] = dt.x + dt.y;
+          }
+        }
+        float sum = reduce_rows<LPR, N>(v, l);
+        if (!BWD || l < LPR / 2) sum = rsqrtf(sum * (1.f / D) + A.eps);
+        gather_rows<LPR, N>(sum, v, l);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const uint32_t row = row_of(n, i0 + i);
+          const bool in = row < static_cast<uint32_t>(A.rows);
+          // a position outside the table: NaN
+          const float r =
+              p0[i0 + i] >= 0 && p0[i0 + i] < A.n_pos ? v[i] : __int_as_float(0x7fffffff);
+          const float2 r2 = make_float2(r, r);
+          Elems y;
+          if constexpr (!BWD) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 xa = mul2(x[i].a[e], w.a[e]), xb = mul2(x[i].b[e], w.b[e]);
+              y.a[e] = mul2(fma2(xa, R[i0 + i].c[e], mul2(neg2(xb), R[i0 + i].s[e])), r2);
+              y.b[e] = mul2(fma2(xb, R[i0 + i].c[e], mul2(xa, R[i0 + i].s[e])), r2);
+            }
+          } else {
+            const float dot = -v[NB + i] * r * (1.f / D);
+            const float2 d2 = make_float2(dot, dot);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 xa = mul2(x[i].a[e], r2), xb = mul2(x[i].b[e], r2);
+              if (in) {
+                acc.a[e] = fma2(z[i].a[e], xa, acc.a[e]);
+                acc.b[e] = fma2(z[i].b[e], xb, acc.b[e]);
+              }
+              y.a[e] = mul2(r2, fma2(xa, d2, mul2(z[i].a[e], w.a[e])));
+              y.b[e] = mul2(r2, fma2(xb, d2, mul2(z[i].b[e], w.b[e])));
+            }
+          }
+          if (in) write_row<ADJ>(A.out + static_cast<size_t>(row) * D, P, y);
+        }
+      }
+    }
+  }
+  if constexpr (BWD) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 pr = e < 4 ? acc.a[(e >> 1) & 1] : acc.b[(e >> 1) & 1];
+      float f = e & 1 ? pr.y : pr.x;
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+      if (sub == 0) red[warp][P.col(e >= 4, e & 3)] = f;
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < 2 * D; x += kNormThreads) {
+      float s = 0.f;
+      if (x / D == A.which)
+        for (int i = 0; i < kNormWarps; ++i) s += red[i][x % D];
+      A.part[static_cast<size_t>(blockIdx.x) * 2 * D + x] = s;
+    }
+  }
+}
+
 // dw[x] = sum of the CTAs' parts: 32 interleaved fp64 sums, joined in order. One launch of a few
 // CTAs, so each thread has all its loads in flight at once.
 __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* __restrict__ part, int n,
@@ -419,61 +601,125 @@ NormArgs args_of(const NormLaunch& L) {
   A.ok = static_cast<__nv_bfloat16*>(L.ok);
   A.part = L.part;
   A.T = L.T; A.Hq = L.Hq; A.Hkv = L.Hkv; A.n_pos = L.n_pos; A.rot = L.rot;
-  A.qchunks = (L.Hq + chunk_rows(L.d) - 1) / chunk_rows(L.d);
-  A.chunks = A.qchunks + (L.Hkv + chunk_rows(L.d) - 1) / chunk_rows(L.d);
   A.eps = L.eps;
   return A;
 }
 
-// CTAs: one per SM, at least a warp for every chunk of a token, and no more than there are units.
-int norm_ctas(int chunks, long long T) {
-  const long long all = (T * chunks + kNormWarps - 1) / kNormWarps;
-  const long long most = kNumSms;
-  return static_cast<int>(std::max<long long>(std::min(all, most),
-                                              (chunks + kNormWarps - 1) / kNormWarps));
+// Where a tensor's heads leave chunks partly empty and there are tokens enough that a second launch
+// does not matter, its rows go through the kernel that packs them. Measured by tokens : by rows, heads
+// of 128: 51739 tokens of 4 / 1 heads 57 : 36 us (floor 21), gradients 99 : 57 (31); 16 / 2 heads
+// 93 : 83 (74), gradients 144 : 123 (110); 5000 tokens of 4 / 1 heads 5.8 : 7.0, gradients 17 : 12.
+bool packed(int H, int d, int T, bool bwd) {
+  return H < chunk_rows(d) && T >= (bwd ? 4096 : 16384);
+}
+int chunks_of(int H, int d) { return (H + chunk_rows(d) - 1) / chunk_rows(d); }
+
+// What a call launches: the kernel by tokens for q and / or k, the kernel by rows for the others.
+struct Launches {
+  int qchunks, kchunks;       // by tokens
+  bool q_rows, k_rows;        // by rows
+  int ctas, q_ctas, k_ctas;   // one per SM at most (by rows, forward: two, whose rings both fit), a
+                              // warp for every chunk of a token at least
+};
+Launches launches_of(int Hq, int Hkv, int d, int T, bool bwd) {
+  Launches N{};
+  N.q_rows = packed(Hq, d, T, bwd);
+  N.k_rows = packed(Hkv, d, T, bwd);
+  N.qchunks = N.q_rows ? 0 : chunks_of(Hq, d);
+  N.kchunks = N.k_rows ? 0 : chunks_of(Hkv, d);
+  auto fit = [](long long chunks, int per_sm) {
+    return static_cast<int>(
+        std::min<long long>((chunks + kNormWarps - 1) / kNormWarps, per_sm * kNumSms));
+  };
+  const int c = N.qchunks + N.kchunks;
+  if (c)
+    N.ctas = std::max(fit(static_cast<long long>(T) * c, 1), (c + kNormWarps - 1) / kNormWarps);
+  const int rows = chunk_rows(d);
+  if (N.q_rows) N.q_ctas = fit((static_cast<long long>(T) * Hq + rows - 1) / rows, bwd ? 1 : 2);
+  if (N.k_rows) N.k_ctas = fit((static_cast<long long>(T) * Hkv + rows - 1) / rows, bwd ? 1 : 2);
+  return N;
 }
 
-template <int D, bool ADJ, bool BWD>
-cudaError_t launch(const NormArgs& A, int ctas, cudaStream_t s) {
-  static std::atomic<int> done[64];
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<int> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(qk_norm_rope_kernel<D, ADJ, BWD>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, norm_smem(BWD));
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_relaxed);
+  return e;
+}
+
+template <int D, bool ADJ, bool BWD>
+cudaError_t launch(const NormLaunch& L, cudaStream_t s) {
+  const Launches N = launches_of(L.Hq, L.Hkv, D, L.T, BWD);
+  NormArgs A = args_of(L);
+  if (N.ctas) {
+    static std::atomic<int> done[64];
+    cudaError_t e = allow_smem(qk_norm_rope_kernel<D, ADJ, BWD>, norm_smem(BWD), done);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_relaxed);
+    A.qchunks = N.qchunks;
+    A.chunks = N.qchunks + N.kchunks;
+    e = launch_early(qk_norm_rope_kernel<D, ADJ, BWD>, dim3(static_cast<unsigned>(N.ctas)),
+                     kNormThreads, norm_smem(BWD), 1, s, A);
+    if (e != cudaSuccess) return e;
   }
-  return launch_early(qk_norm_rope_kernel<D, ADJ, BWD>, dim3(static_cast<unsigned>(ctas)),
-                      kNormThreads, norm_smem(BWD), 1, s, A);
+  for (int which = 0; which < 2; ++which) {
+    if (!(which ? N.k_rows : N.q_rows)) continue;
+    constexpr int smem = kNormWarps * (BWD ? 8 : 6) * kChunkBytes;
+    static std::atomic<int> done[64];
+    cudaError_t e = allow_smem(norm_rope_rows_kernel<D, ADJ, BWD>, smem, done);
+    if (e != cudaSuccess) return e;
+    RowsArgs R{};
+    R.x = which ? A.k : A.q;
+    R.dy = which ? A.dyk : A.dyq;
+    R.ld = which ? A.k_ld : A.q_ld;
+    R.w = which ? A.wk : A.wq;
+    R.rope = A.rope; R.pos = A.pos;
+    R.out = which ? A.ok : A.oq;
+    R.H = which ? L.Hkv : L.Hq;
+    R.rows = L.T * R.H;
+    R.n_pos = A.n_pos; R.rot = A.rot; R.eps = A.eps; R.which = which;
+    int lg = 0;
+    while ((1 << lg) < R.H) ++lg;
+    if (R.H > 1) {
+      R.magic = static_cast<uint32_t>((1ull << (31 + lg)) / R.H + 1);
+      R.shift = lg - 1;
+    }
+    R.part = BWD ? L.part + static_cast<size_t>(N.ctas + (which ? N.q_ctas : 0)) * 2 * D : nullptr;
+    e = launch_early(norm_rope_rows_kernel<D, ADJ, BWD>,
+                     dim3(static_cast<unsigned>(which ? N.k_ctas : N.q_ctas)), kNormThreads, smem,
+                     1, s, R);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 template <bool BWD>
-cudaError_t launch_any(const NormLaunch& L, int ctas, cudaStream_t s) {
-  const NormArgs A = args_of(L);
+cudaError_t launch_any(const NormLaunch& L, cudaStream_t s) {
   if (L.d == 64)
-    return L.adjacent ? launch<64, true, BWD>(A, ctas, s) : launch<64, false, BWD>(A, ctas, s);
-  return L.adjacent ? launch<128, true, BWD>(A, ctas, s) : launch<128, false, BWD>(A, ctas, s);
-}
-
-int chunks_of(int Hq, int Hkv, int d) {
-  const int rows = chunk_rows(d);
-  return (Hq + rows - 1) / rows + (Hkv + rows - 1) / rows;
+    return L.adjacent ? launch<64, true, BWD>(L, s) : launch<64, false, BWD>(L, s);
+  return L.adjacent ? launch<128, true, BWD>(L, s) : launch<128, false, BWD>(L, s);
 }
 
 }  // namespace
 
-int qk_norm_bwd_ctas(int Hq, int Hkv, int d, int T) {
-  return norm_ctas(chunks_of(Hq, Hkv, d), T);
+int qk_norm_bwd_parts(int Hq, int Hkv, int d, int T) {
+  const Launches N = launches_of(Hq, Hkv, d, T, true);
+  return N.ctas + N.q_ctas + N.k_ctas;
 }
 
-cudaError_t launch_qk_norm(const NormLaunch& L, cudaStream_t s) {
-  return launch_any<false>(L, norm_ctas(chunks_of(L.Hq, L.Hkv, L.d), L.T), s);
+int qk_norm_bwd_max_parts(int Hq, int Hkv, int d) {
+  // by tokens at most one per SM (or what the chunks of one token take), by rows one per SM for each
+  return std::max(kNumSms, (chunks_of(Hq, d) + chunks_of(Hkv, d) + kNormWarps - 1) / kNormWarps) +
+         2 * kNumSms;
 }
 
-cudaError_t launch_qk_norm_bwd(const NormLaunch& L, int ctas, cudaStream_t s) {
-  return launch_any<true>(L, ctas, s);
+cudaError_t launch_qk_norm(const NormLaunch& L, cudaStream_t s) { return launch_any<false>(L, s); }
+
+cudaError_t launch_qk_norm_bwd(const NormLaunch& L, cudaStream_t s) {
+  return launch_any<true>(L, s);
 }
 
 cudaError_t launch_qk_norm_dw(const float* part, int n, int d, float* dwq, float* dwk,

@@ -54,6 +54,12 @@ CASES = [  # T, hq, hkv, d, rot, interleaved, fused
     (2000, 4, 1, 128, 48, False, False),
     (20000, 32, 8, 128, 128, False, True),  # many chunks a warp
     (7000, 20, 20, 64, 48, True, False),
+    (16384, 4, 1, 128, 128, False, True),   # few heads, many tokens: rows packed across tokens
+    (20001, 1, 3, 128, 64, True, False),
+    (4096, 4, 1, 128, 128, False, False),   # the gradients' alone
+    (30011, 5, 2, 64, 64, False, True),
+    (17000, 16, 2, 128, 32, False, True),   # q by tokens, k by rows
+    (16501, 7, 17, 64, 32, True, True),     # and the other way round
 ]
 
 
@@ -121,26 +127,28 @@ def test_no_rows(moba):
     assert not dwq.any() and not dwk.any()
 
 
-def test_position_outside_the_table_is_nan_in_that_token_only(moba):
-    q, k, wq, wk, rope, pos = _inputs(moba, 6, 4, 2, 128, 64, False, n_pos=50)
+@pytest.mark.parametrize("T", [6, 17003])
+def test_position_outside_the_table_is_nan_in_that_token_only(moba, T):
+    q, k, wq, wk, rope, pos = _inputs(moba, T, 4, 2, 128, 64, False, n_pos=50)
     pos[2], pos[4] = 50, -1
     yq, yk = moba.moba_qk_norm_rope(q, k, wq, wk, rope, pos)
     for y in (yq, yk):
         bad = y.isnan().flatten(1)
-        assert bad[[2, 4]].all() and not bad[[0, 1, 3, 5]].any()
+        assert bad[[2, 4]].all() and not bad[[0, 1, 3, 5]].any() and not bad[6:].any()
 
 
-def test_in_place_zero_rows_and_rows_behind_the_call(moba):
+@pytest.mark.parametrize("T", [9, 16501])
+def test_in_place_zero_rows_and_rows_behind_the_call(moba, T):
     """Packed outputs may be the inputs; a row of zeros stays zero; the tokens behind the call's
     are left as they were."""
-    q, k, wq, wk, rope, pos = _inputs(moba, 9, 4, 2, 64, 64, False, seed=2)
+    q, k, wq, wk, rope, pos = _inputs(moba, T, 4, 2, 64, 64, False, seed=2)
     q[3] = 0
     want = moba.moba_qk_norm_rope(q, k, wq, wk, rope, pos)
     assert not want[0][3].any()
-    qq, kk = torch.full((12, 4, 64), 5.0, device="cuda").bfloat16(), k.clone()
-    qq[:9] = q
-    moba.moba_qk_norm_rope(qq[:9], kk, wq, wk, rope, pos, q_out=qq[:9], k_out=kk)
-    assert torch.equal(qq[:9], want[0]) and torch.equal(kk, want[1]) and (qq[9:] == 5.0).all()
+    qq, kk = torch.full((T + 3, 4, 64), 5.0, device="cuda").bfloat16(), k.clone()
+    qq[:T] = q
+    moba.moba_qk_norm_rope(qq[:T], kk, wq, wk, rope, pos, q_out=qq[:T], k_out=kk)
+    assert torch.equal(qq[:T], want[0]) and torch.equal(kk, want[1]) and (qq[T:] == 5.0).all()
     dyq, dyk = torch.randn_like(q), torch.randn_like(k)
     want = moba.moba_qk_norm_rope_bwd(q, k, wq, wk, rope, pos, dyq, dyk)
     got = moba.moba_qk_norm_rope_bwd(q, k, wq, wk, rope, pos, dyq, dyk, dq=dyq, dk=dyk)
