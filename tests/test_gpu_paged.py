@@ -588,6 +588,60 @@ def test_two_graphs_at_once(moba):
         assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
 
 
+def test_captured_behind_copies_and_a_join_of_streams(moba):
+    """A captured step whose first call comes behind a copy, and whose attention comes behind the join
+    of two captured streams."""
+    lens = [700, 90]
+    S = Setup(moba, lens, 2, 64, 16, "bf16", 64)
+    _fill(S, lens)
+    src = torch.randn((2, 4, 64), generator=_gen(2), device="cuda").bfloat16()
+    q = torch.zeros_like(src)
+    wq, wk = torch.rand(64, device="cuda") + 0.5, torch.rand(64, device="cuda") + 0.5
+    rope, pos = moba.rope_table(100, 64), torch.zeros(2, dtype=torch.int32, device="cuda")
+    k = torch.randn((2, 2, 64), generator=_gen(4), device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+
+    def step():
+        q.copy_(src)
+        yq, _ = moba.moba_qk_norm_rope(q, k, wq, wk, rope, pos)
+        cur = torch.cuda.current_stream()
+        side.wait_stream(cur)
+        with torch.cuda.stream(side):
+            a = moba.moba_paged_attn_fwd(S.cache, yq)
+        b = moba.moba_paged_decode_fwd(S.cache, yq, 3)
+        cur.wait_stream(side)
+        return a + b + moba.moba_paged_decode_fwd(S.cache, a[0], 2)
+
+    want = step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(5):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_queries_of_any_size(moba):
+    """e4m3: query rows of zeros, of subnormal and of huge values (each row has a scaling of its
+    own)."""
+    n, d = 300, 64
+    S = Setup(moba, [n] * 4, 1, d, 16, "e4m3")
+    _fill(S, [n] * 4)
+    q = torch.randn((4, 2, d), generator=_gen(6), device="cuda")
+    q *= torch.tensor([0.0, 2.0 ** -128, 2.0 ** -60, 2.0 ** 100], device="cuda")[:, None, None]
+    q = q.bfloat16()
+    rows = [S.rows(s, n) for s in range(4)]
+    for scale, use in ((0.125, [0, 1, 2]), (2.0 ** -100, [0, 1, 2, 3])):
+        o, lse = moba.moba_paged_attn_fwd(S.cache, q, scale=scale)
+        want = cref.cached_attention(q, [r[0] for r in rows], [r[1] for r in rows], [n] * 4, 1,
+                                     scale)
+        pick = lambda w: (w[0][use], w[1][:, use], None, w[3][use], w[4][:, use])  # noqa: E731
+        _close(o[use], lse[:, use], pick(want), _w("e4m3"))
+
+
 def test_prefill_then_decode(moba):
     """A run of the operators as a model's layer uses them: norm + rotary over the prompt, MoBA
     prefill, the cache written; then tokens one at a time through the paged cache, each against
