@@ -533,13 +533,16 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          s = s > 0.f ? s * ex2(r[nt][j] - top) : 0.f;
+          if (s != 0.f) s *= ex2(r[nt][j] - top);  // a lane without keys: 0, and r = -inf
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         mul = s > 0.f ? 1.f / s : 0.f;
         if (FP8 && s > 0.f) mul *= ex2(m[nt][j] - 15.f - top);
-        if (bad) mul = top = nan;
+        // The maxima pass over a NaN logit, the sum keeps it. A row that sees a key and ends
+        // without a sum had logits of -inf alone.
+        const bool gone = bad || s != s || (whole && lim[nt][j] > 0 && !(s > 0.f));
+        if (gone) mul = top = nan;
         const int col = nt * 8 + 2 * c + j, rr = id.rt * kRows + col;
         if (rr >= R) continue;
         if (whole) {
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
           }
           if (n4 == 0)
             A.lse[static_cast<size_t>(h) * A.nseq * A.rows + row] =
-                bad ? nan : s > 0.f ? (top + log2f(s)) * 0.69314718055994531f : -INFINITY;
+                gone ? nan : s > 0.f ? (top + log2f(s)) * 0.69314718055994531f : -INFINITY;
         } else {
           float* dst = po + col * D;
 #pragma unroll
@@ -812,7 +815,7 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
   float* slices = reinterpret_cast<float*>(smem + kRows * D * 4 + kRows * 8);  // [warps][D]
   const Seg js = seg_of(A, seg0);
   bool over;
-  seq_len(A, js.s, &over);
+  const int jlen = seq_len(A, js.s, &over);
   if (SPARSE) over |= A.seg_tiles[seg0] < 0;
   const int crank = blockIdx.x % A.join;
   const int nrow = min(kRows, A.rows * A.group - js.rt * kRows);
@@ -852,6 +855,8 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    // a row with a position and without a sum: logits of -inf alone
+    nan |= !(sum > 0.f) && jlen - A.rows + (js.rt * kRows + row) / A.group >= 0;
 #pragma unroll
     for (int e = 0; e < PER; ++e) o[e] = 0.f;
     for (int i0 = slice * each; i0 < (slice + 1) * each; i0 += 8) {
@@ -903,7 +908,8 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
 // joined in a fixed order. Bound by latency: two dependent loads (the segment's description, then
 // the partials), so a warp has kMergeBatch partials in flight at once and the host gives a CTA
 // more warps the fewer segments share the partials. Rows without keys get o = 0, lse = -inf; a
-// row whose sequence names a page outside the pool gets NaN.
+// row whose sequence names a page outside the pool gets NaN, and so does one whose query is not
+// finite.
 constexpr int kMergeBatch = 8;
 constexpr int kMergeWarps = 16;  // at most
 
@@ -953,7 +959,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
     }
 #pragma unroll
     for (int x = 0; x < kMergeBatch; ++x) {
-      bad |= !(ml[x].x <= FLT_MAX);  // NaN: a bad page
+      bad |= !(ml[x].x <= FLT_MAX);  // NaN: a bad page or a logit that is NaN
       if (ml[x].y > 0.f) {
         const float mn = fmaxf(m, ml[x].x), a = exp2f(m - mn), b = exp2f(ml[x].x - mn) * ml[x].y;
         l = fmaf(l, a, b);
@@ -978,6 +984,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
   }
   for (int w = 0; w < NW; ++w)
     if (sl[w] > 0.f) Lsum = fmaf(exp2f(sm[w] - M), sl[w], Lsum);
+  // a row with a position and without a sum: logits of -inf alone
+  any_bad |= !(Lsum > 0.f) && L - A.rows + r >= 0;
   const float inv = any_bad ? __int_as_float(0x7fffffff) : Lsum > 0.f ? 1.f / Lsum : 0.f;
   for (int x = threadIdx.x; x < D; x += blockDim.x) {
     float o = 0.f;

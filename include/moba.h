@@ -296,7 +296,8 @@ int moba_cache_read(const moba_paged_cache* cache, const int32_t* cu_seqlens_dev
  * o: bf16 [nseq * rows_per_seq, Hq, d]; lse: fp32 [Hq, nseq * rows_per_seq]. A row without a
  * position (seq_lens[s] < rows_per_seq) gives o = 0, lse = -inf and -1s. A sequence that needs a
  * page outside the pool, or more pages than max_pages, gives NaN in its rows of o and lse; the
- * other sequences' rows are right. The same call on the same contents gives the same bits; how a
+ * other sequences' rows are right. A query row that is not finite gives NaN in that row's o and lse
+ * (its routing ranks NaN scores last). The same call on the same contents gives the same bits; how a
  * sequence is cut over the SMs depends on all lengths of the call, so the last bits of its rows may
  * differ in another batch. Cached values that a row must not see may be anything in rows at
  * or behind seq_lens[s]; values of cached rows are to be finite.

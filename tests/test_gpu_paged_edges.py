@@ -1,0 +1,70 @@
+"""Attention over a paged cache where a result is easily wrong without looking wrong: queries that
+are not finite, values of tiny scales. Tolerances as in test_gpu_paged.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ref as cref
+from tests.test_gpu_paged import Setup, _close, _cu, _gen, _w, moba  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# lens, hq, hkv, d, page: how the rows of a segment come together
+CUTS = [
+    ([1000, 2], 8, 2, 128, 64),          # a cluster joins each segment
+    ([30000, 0, 1], 4, 2, 64, 64),       # many warps share a segment, then the merge
+    ([50, 60, 1, 70] * 60, 4, 2, 64, 16),  # mostly one warp per segment
+]
+
+
+def _positive_first(S, lens, seed=1):
+    """Appends random rows whose keys have a positive first element; returns nothing."""
+    g = _gen(seed)
+    k = torch.randn((sum(lens), S.hkv, S.d), generator=g, device="cuda")
+    k[..., 0] = k[..., 0].abs() + 0.5
+    v = torch.randn((sum(lens), S.hkv, S.d), generator=g, device="cuda")
+    S.moba.moba_cache_append(S.cache, k.bfloat16(), v.bfloat16(),
+                             torch.tensor(_cu(lens), dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("topk", [0, 3])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("cut", CUTS, ids=lambda c: f"{len(c[0])}x{max(c[0])}")
+def test_a_query_that_is_not_finite_is_nan_in_its_row_alone(moba, cut, kv, topk):  # noqa: F811
+    """A NaN, an infinity, and an infinity that makes every logit -inf: by the formula the row is
+    NaN (o and lse), unless it has no position, then it has no keys and is 0, -inf; the other
+    rows, of the same kv head too, are right."""
+    lens, hq, hkv, d, page = cut
+    rows, block = 2, 128
+    S = Setup(moba, lens, hkv, d, page, kv, block)
+    _positive_first(S, lens)
+    n = len(lens) * rows
+    q = torch.randn((n, hq, d), generator=_gen(7), device="cuda").bfloat16()
+    clean = q.clone()
+    bad = np.zeros((n, hq), bool)
+    last = n - 1
+    for at, h, x in ((1, 0, float("nan")), (1, hq - 1, float("inf")), (0, 1, float("-inf")),
+                     (last, 2, float("nan")), (last - 1, 1, float("nan"))):
+        q[at, h, 0] = x
+        bad[at, h] = True
+    if topk:
+        o, lse = moba.moba_paged_decode_fwd(S.cache, q, topk, rows_per_seq=rows)
+    else:
+        o, lse = moba.moba_paged_attn_fwd(S.cache, q, rows_per_seq=rows)
+    kv_rows = [S.rows(s, x) for s, x in enumerate(lens)]
+    sums = [cref.f64(S.sums[S.table[s, :-(-x // page):block // page].long()])
+            for s, x in enumerate(lens)] if topk else None
+    want = list(cref.cached_attention(clean, [x[0] for x in kv_rows], [x[1] for x in kv_rows],
+                                      lens, rows, d ** -0.5, sums, block, topk))
+    here = np.array([lens[i // rows] - rows + i % rows >= 0 for i in range(n)])
+    for i, h in zip(*np.nonzero(bad)):
+        if here[i]:
+            assert o[i, h].isnan().all() and lse[h, i].isnan(), (i, h)
+        else:
+            assert not o[i, h].any() and torch.isneginf(lse[h, i]), (i, h)
+    keep = torch.from_numpy(~bad).cuda()
+    zero = lambda x, m: torch.where(m, x, torch.zeros_like(x))  # noqa: E731
+    for x in (want[0], want[3]):
+        x[bad] = 0
+    want[1][bad.T] = 0
+    _close(zero(o, keep[..., None]), zero(lse, keep.T), want, _w(kv))
