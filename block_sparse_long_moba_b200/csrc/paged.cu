@@ -538,7 +538,13 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         mul = s > 0.f ? 1.f / s : 0.f;
-        if (FP8 && s > 0.f) mul *= ex2(m[nt][j] - 15.f - top);
+        // e4m3: times 2^(m - 15 - top), down to 2^-141: half of the exponent in each of two factors,
+        // as the whole would be 0 where the values' scales are all small
+        float lead = 1.f;
+        if (FP8 && s > 0.f) {
+          lead = ex2(0.5f * (m[nt][j] - 15.f - top));
+          mul *= lead;
+        }
         // The maxima pass over a NaN logit, the sum keeps it. A row that sees a key and ends
         // without a sum had logits of -inf alone.
         const bool gone = bad || s != s || (whole && lim[nt][j] > 0 && !(s > 0.f));
@@ -552,8 +558,8 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
 #pragma unroll
           for (int ds = 0; ds < KS; ++ds) {
             const int d0 = ds * 16 + (FP8 ? 2 * n4 : n4), d1 = d0 + (FP8 ? 1 : 8);
-            dst[d0] = __float2bfloat16_rn(acc[ds][nt][j] * mul);
-            dst[d1] = __float2bfloat16_rn(acc[ds][nt][2 + j] * mul);
+            dst[d0] = __float2bfloat16_rn(acc[ds][nt][j] * lead * mul);
+            dst[d1] = __float2bfloat16_rn(acc[ds][nt][2 + j] * lead * mul);
           }
           if (n4 == 0)
             A.lse[static_cast<size_t>(h) * A.nseq * A.rows + row] =
@@ -563,8 +569,8 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
 #pragma unroll
           for (int ds = 0; ds < KS; ++ds) {
             const int d0 = ds * 16 + (FP8 ? 2 * n4 : n4), d1 = d0 + (FP8 ? 1 : 8);
-            dst[d0] = acc[ds][nt][j] * mul;
-            dst[d1] = acc[ds][nt][2 + j] * mul;
+            dst[d0] = acc[ds][nt][j] * lead * mul;
+            dst[d1] = acc[ds][nt][2 + j] * lead * mul;
           }
           if (n4 == 0) pml[col] = make_float2(top, s);
         }

@@ -68,3 +68,23 @@ def test_a_query_that_is_not_finite_is_nan_in_its_row_alone(moba, cut, kv, topk)
         x[bad] = 0
     want[1][bad.T] = 0
     _close(zero(o, keep[..., None]), zero(lse, keep.T), want, _w(kv))
+
+
+@pytest.mark.parametrize("n", [40, 700, 20000])  # one warp's tile, a joined segment, a merged one
+@pytest.mark.parametrize("exponent", [-121, -115, -100])
+def test_values_of_tiny_scales(moba, n, exponent):  # noqa: F811
+    """e4m3 values near 2^exponent: scale bytes down to 1. The output is a normal bf16 number."""
+    hkv, d = 1, 64
+    S = Setup(moba, [n], hkv, d, 16, "e4m3")
+    g = _gen(17)
+    k = torch.randn((n, hkv, d), generator=g, device="cuda").bfloat16()
+    v = (torch.randn((n, hkv, d), generator=g, device="cuda").sign()
+         * (1 + torch.rand((n, hkv, d), generator=g, device="cuda"))).double()
+    v = (v * 2.0 ** exponent).bfloat16()
+    v[..., ::2] = v[..., ::2].abs()  # columns whose mean does not vanish
+    moba.moba_cache_append(S.cache, k, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    q = torch.randn((1, 2, d), generator=g, device="cuda").bfloat16()
+    kk, vv = S.rows(0, n)
+    o, lse = moba.moba_paged_attn_fwd(S.cache, q)
+    assert (o[..., ::2] > 2.0 ** (exponent - 1)).all()
+    _close(o, lse, cref.cached_attention(q, [kk], [vv], [n], 1, d ** -0.5), _w("e4m3"))
