@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(kCacheThreads, 4) cache_append_kernel(const Ap
   const int unit = blockIdx.x / CS;
   wait_previous_kernel();
   const int s = last_not_above(C.nseq, unit, [&](int x) {
-    return first_unit(__ldg(A.cuq + x), x, C.B);
+    return first_unit(A.cuq[x], x, C.B);
   });
-  const int c0 = __ldg(A.cuq + s), c1 = __ldg(A.cuq + s + 1);
-  const int L = __ldg(C.seq_lens + s);
+  const int c0 = A.cuq[s], c1 = A.cuq[s + 1];
+  const int L = C.seq_lens[s];
   // host and device copies may disagree: rows outside the buffers are never touched
   const int n = (c0 >= 0 && c1 >= c0 && c1 <= A.Tq) ? c1 - c0 : 0;
   const int p0 = max(L - n, 0);  // first new position
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kCacheThreads, 4) cache_append_kernel(const Ap
 #pragma unroll
   for (int i = 0; i < kAppendStages - 1; ++i) issue(i);
   int x = a0 + tt, stage = 0;
-  auto page_of = [&](int u) { return mine && u < a1 ? __ldg(pages + (u >> C.page_log)) : -1; };
+  auto page_of = [&](int u) { return mine && u < a1 ? pages[u >> C.page_log] : -1; };
   int pid = page_of(x);
   for (int it = 0; it < iters; ++it, x += TP) {
     issue(stage == 0 ? kAppendStages - 1 : stage - 1);
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kCacheThreads, 4) cache_append_kernel(const Ap
   }
   cluster.sync();
   if (rank == 0) {
-    const int home = __ldg(pages + ((static_cast<long long>(b) * C.B) >> C.page_log));
+    const int home = pages[(static_cast<long long>(b) * C.B) >> C.page_log];
     if (home >= 0 && home < C.num_pages) {
       const bool fresh = static_cast<long long>(b) * C.B >= p0;  // the block begins with new rows
       for (int x = threadIdx.x; x < nh * D; x += kCacheThreads) {
@@ -280,17 +280,16 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const ReadArg
   const int nr = min(kReadRows, A.T - r0);
   wait_previous_kernel();
   if (threadIdx.x < 32) {  // kReadRows rows, one per lane
-    const int s0 = last_not_above(C.nseq, r0, [&](int x) { return __ldg(A.cu + x); });
+    const int s0 = last_not_above(C.nseq, r0, [&](int x) { return A.cu[x]; });
     const int r = r0 + threadIdx.x;
     int lo = s0;  // the rows of a CTA mostly lie in one sequence
-    while (lo + 1 < C.nseq && __ldg(A.cu + lo + 1) <= r) ++lo;
-    const long long u = static_cast<long long>(r) - __ldg(A.cu + lo);
+    while (lo + 1 < C.nseq && A.cu[lo + 1] <= r) ++lo;
+    const long long u = static_cast<long long>(r) - A.cu[lo];
     long long x = -1;
-    if (r < A.T && u >= 0 && u < __ldg(C.seq_lens + lo) && r < __ldg(A.cu + lo + 1)) {
+    if (r < A.T && u >= 0 && u < C.seq_lens[lo] && r < A.cu[lo + 1]) {
       x = -2;
       if ((u >> C.page_log) < C.max_pages) {
-        const int pid = __ldg(C.page_table + static_cast<size_t>(lo) * C.max_pages +
-                              (u >> C.page_log));
+        const int pid = C.page_table[static_cast<size_t>(lo) * C.max_pages + (u >> C.page_log)];
         if (pid >= 0 && pid < C.num_pages)
           x = ((static_cast<long long>(pid) * C.G) << C.page_log) +
               (u & ((1 << C.page_log) - 1));
@@ -321,8 +320,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const ReadArg
             const uint2 b = __ldcs(reinterpret_cast<const uint2*>(C.v + row * D) + l);
             kr[i].x = a.x; kr[i].y = a.y;
             vr[i].x = b.x; vr[i].y = b.y;
-            kf[i] = __uint_as_float(static_cast<uint32_t>(__ldg(C.ks + row)) << 23);
-            vf[i] = __uint_as_float(static_cast<uint32_t>(__ldg(C.vs + row)) << 23);
+            kf[i] = __uint_as_float(static_cast<uint32_t>(C.ks[row]) << 23);
+            vf[i] = __uint_as_float(static_cast<uint32_t>(C.vs[row]) << 23);
           } else {
             kr[i] = __ldcs(reinterpret_cast<const uint4*>(C.k + row * D * 2) + l);
             vr[i] = __ldcs(reinterpret_cast<const uint4*>(C.v + row * D * 2) + l);

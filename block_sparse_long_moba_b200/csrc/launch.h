@@ -169,7 +169,9 @@ constexpr int kNumSms = 148;
 
 // Launch whose CTAs may be scheduled while the kernel before it on the stream drains: the kernel
 // calls wait_previous_kernel() before it reads or writes anything, so that the order of the stream
-// is kept and only the launch latency is hidden. cluster: CTAs of a cluster along x.
+// is kept and only the launch latency is hidden. Such a kernel reads with plain loads alone: the
+// read-only path (__ldg, __restrict__) is for memory that nothing writes while the kernel is resident,
+// and its loads are not ordered behind the wait. cluster: CTAs of a cluster along x.
 template <class... K, class... A>
 cudaError_t launch_early(void (*kernel)(K...), dim3 grid, int block, size_t smem, int cluster,
                          cudaStream_t s, A... args) {

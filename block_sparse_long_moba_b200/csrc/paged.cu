@@ -173,7 +173,7 @@ __device__ __forceinline__ Seg seg_of(const PagedArgs& A, int seg) {
 // Cached tokens of sequence s, cut to what its row of the page table can hold (a longer sequence
 // is reported as bad by the callers).
 __device__ __forceinline__ int seq_len(const PagedArgs& A, int s, bool* over) {
-  const int L = max(__ldg(A.seq_lens + s), 0);
+  const int L = max(A.seq_lens[s], 0);
   const long long cap = static_cast<long long>(A.max_pages) << A.page_log;
   *over = L > cap;
   return static_cast<int>(min(static_cast<long long>(L), cap));
@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
     my_pid = 0;
     bool bad = l_over;
     if (lane < KT / 16 && lane * 16 < nk) {
-      my_pid = __ldg(A.page_table + static_cast<size_t>(l_id.s) * A.max_pages +
-                     ((kpos + lane * 16) >> A.page_log));
+      my_pid = A.page_table[static_cast<size_t>(l_id.s) * A.max_pages +
+                             ((kpos + lane * 16) >> A.page_log)];
       if (my_pid < 0 || my_pid >= A.num_pages) {
         bad = true;
         my_pid = -1;
@@ -1157,7 +1157,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
   // eight lanes per block: this group's blocks are first, first + stride, ...
   const int first = (rank * kGateWarps + warp) * 4 + (lane >> 3), stride = CS * kGateWarps * 4;
   auto page_of = [&](int j) {
-    return j < A.nb_cap ? __ldg(pages + ((static_cast<long long>(j) * A.B) >> A.page_log)) : -1;
+    return j < A.nb_cap ? pages[(static_cast<long long>(j) * A.B) >> A.page_log] : -1;
   };
   int pid[U];
 #pragma unroll
@@ -1193,7 +1193,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) paged_gate_kernel(const Paged
             A.sums + (static_cast<size_t>(ok ? pid[u] : 0) * A.G + id.g) * D);
 #pragma unroll
         for (int x = 0; x < NV; ++x)
-          c[u][x] = in && ok ? __ldg(src + l8 + 8 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
+          c[u][x] = in && ok ? src[l8 + 8 * x] : make_float4(0.f, 0.f, 0.f, 0.f);
         if (in && !ok) sbad = 1;
       }
 #pragma unroll

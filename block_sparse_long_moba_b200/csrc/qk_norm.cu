@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) qk_norm_rope_kernel(const Nor
     // lane x fetches the position of the warp's unit n0 + x; 32 units at a time
     auto positions = [&](int n0) {
       const long long t = t0 + static_cast<long long>(n0 + lane) * step;
-      return t < A.T ? __ldg(A.pos + t) : -1;
+      return t < A.T ? A.pos[t] : -1;
     };
     const int units = (A.T - t0 + step - 1) / step;
     int pos = positions(0);
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kNormThreads, BWD ? 1 : 2) norm_rope_rows_kern
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
         const uint32_t r = row_of(n, i);
-        p[i] = n < units && r < static_cast<uint32_t>(A.rows) ? __ldg(A.pos + token_of(r)) : -1;
+        p[i] = n < units && r < static_cast<uint32_t>(A.rows) ? A.pos[token_of(r)] : -1;
       }
     };
     auto fetch_angles = [&](const int (&p)[kIter], Angle (&R)[kIter]) {
@@ -570,9 +570,8 @@ __global__ void __launch_bounds__(kNormThreads, BWD ? 1 : 2) norm_rope_rows_kern
 
 // dw[x] = sum of the CTAs' parts: 32 interleaved fp64 sums, joined in order. One launch of a few
 // CTAs, so each thread has all its loads in flight at once.
-__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* __restrict__ part, int n,
-                                                          int D, float* __restrict__ dwq,
-                                                          float* __restrict__ dwk) {
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* part, int n, int D,
+                                                          float* dwq, float* dwk) {
   __shared__ double red[32][33];
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5, x = blockIdx.x * 32 + c;
   wait_previous_kernel();
