@@ -271,4 +271,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__bind(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", MOBA_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -4,13 +4,14 @@ Every step of the MoBA forward pass runs in the library's CUDA kernels; PyTorch 
 device memory and the current stream. The functions mirror the C entry points of include/moba.h
 and raise if the library is missing or a call fails — there is no fallback path. The calls around
 the paged cache, which a decode step makes in microseconds, marshal their arguments in csrc/bind.cpp
-where these are plain (on the current stream, all as documented); the checks here handle the rest and
-say what is wrong.
+where these are plain (on the current stream, all as documented) and _bind.so loads; the checks here
+handle the rest and say what is wrong.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -46,7 +47,25 @@ class MobaError(RuntimeError):
 
 
 _lib = None
-_bind = None  # csrc/bind.cpp, once the library is loaded
+_bind = None  # csrc/bind.cpp, once the library is loaded; None where it does not load
+
+
+def _load_bind():
+    """The native argument marshalling, or None with a warning: its calls then go through the checks
+    of this file, with the same results and some microseconds more per call."""
+    try:
+        from . import _bind as bind
+        made_for = bind.torch_version
+    except (ImportError, AttributeError) as e:
+        why = f"is missing or does not load ({e})"
+    else:
+        if made_for == torch.__version__:
+            return bind
+        why = f"was built for torch {made_for}, this is {torch.__version__}"
+    warnings.warn(f"_bind.so {why}; the norm and paged-cache calls take the slower way. Build it "
+                  "with `python -m block_sparse_long_moba_b200.build`", RuntimeWarning,
+                  stacklevel=3)
+    return None
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -58,11 +77,6 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"libmoba.so not found at {path}; build it with "
                           "`python -m block_sparse_long_moba_b200.build`")
-    try:
-        from . import _bind as bind
-    except ImportError as e:
-        raise ImportError(f"the binding's _bind.so is missing or does not load ({e}); build it "
-                          "with `python -m block_sparse_long_moba_b200.build`") from e
     lib = ctypes.CDLL(path)
     P, I, L, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
     lib.moba_status_string.argtypes = [I]
@@ -122,10 +136,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moba_paged_attn_fwd.restype = I
     lib.moba_paged_decode_fwd.argtypes = [P, P, I, I, I, F, P, P, P, P, S, P]
     lib.moba_paged_decode_fwd.restype = I
-    bind.init(*(ctypes.cast(f, P).value for f in (
-        lib.moba_qk_norm_rope, lib.moba_qk_norm_rope_bwd,
-        lib.moba_qk_norm_rope_bwd_workspace_bytes, lib.moba_cache_append, lib.moba_cache_read,
-        lib.moba_paged_attn_fwd, lib.moba_paged_decode_fwd)))
+    bind = _load_bind()
+    if bind is not None:
+        bind.init(*(ctypes.cast(f, P).value for f in (
+            lib.moba_qk_norm_rope, lib.moba_qk_norm_rope_bwd,
+            lib.moba_qk_norm_rope_bwd_workspace_bytes, lib.moba_cache_append,
+            lib.moba_cache_read, lib.moba_paged_attn_fwd, lib.moba_paged_decode_fwd)))
     _lib, _bind = lib, bind
     return lib
 

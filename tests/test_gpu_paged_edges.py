@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import cache_ref as cref
-from tests.test_gpu_paged import Setup, _close, _cu, _gen, _w, moba  # noqa: F401
+from tests.test_gpu_paged import Setup, _close, _cu, _fill, _gen, _w, moba  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,31 @@ def test_values_of_tiny_scales(moba, n, exponent):  # noqa: F811
     o, lse = moba.moba_paged_attn_fwd(S.cache, q)
     assert (o[..., ::2] > 2.0 ** (exponent - 1)).all()
     _close(o, lse, cref.cached_attention(q, [kk], [vv], [n], 1, d ** -0.5), _w("e4m3"))
+
+
+def test_calls_without_the_native_binding(moba, monkeypatch):  # noqa: F811
+    """The same bits where the arguments are marshalled in Python alone."""
+    lens = [300, 70]
+    g = _gen(5)
+    q = torch.randn((2, 4, 64), generator=g, device="cuda").bfloat16()
+    k = torch.randn((2, 2, 64), generator=g, device="cuda").bfloat16()
+    w = torch.rand(64, generator=g, device="cuda") + 0.5
+    rope, pos = moba.rope_table(400, 64), torch.tensor([299, 69], dtype=torch.int32, device="cuda")
+    one = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+
+    def run():
+        S = Setup(moba, lens, 2, 64, 16, "e4m3", 64)
+        S.lens.sub_(1)
+        _fill(S, [x - 1 for x in lens])
+        S.lens.add_(1)
+        y, yk = moba.moba_qk_norm_rope(q, k, w, w, rope, pos)
+        grads = moba.moba_qk_norm_rope_bwd(q, k, w, w, rope, pos, y, yk)
+        moba.moba_cache_append(S.cache, yk, yk, one)
+        cu = _cu(lens)
+        rows = moba.moba_cache_read(S.cache, torch.tensor(cu, dtype=torch.int32, device="cuda"), cu)
+        return (y, yk, *grads, *rows, *moba.moba_paged_attn_fwd(S.cache, y),
+                *moba.moba_paged_decode_fwd(S.cache, y, 3))
+
+    want = run()
+    monkeypatch.setattr(moba, "_bind", None)
+    assert all(torch.equal(a, b) for a, b in zip(run(), want))
