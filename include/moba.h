@@ -242,7 +242,11 @@ int moba_qk_norm_rope_bwd(const void* q, long long q_stride, const void* k, long
  *              64 and of page_size. max_pages * page_size <= 2^30, Hkv <= 1024.
  * Entries of page_table behind a sequence's last page are not used. A page number outside
  * [0, num_pages), or a seq_lens beyond max_pages * page_size, is never dereferenced: the calls
- * below say what becomes of it. Two sequences may share pages that no call writes.
+ * below say what becomes of it. Two sequences may share pages that no call writes. With block_sums a
+ * call that brings rows of a block writes the block's first page too (its sum): sequences that go on
+ * from a common prefix inside a block each need that block's first page for themselves (a copy of the
+ * page, its scales and its row of block_sums), and as ever the page that they write in; the block's
+ * full pages between may stay shared.
  */
 #define MOBA_CACHE_BF16 0
 #define MOBA_CACHE_E4M3 1
@@ -270,7 +274,7 @@ typedef struct {
  *   write the block again from its first row before its sum is used.
  * Rows whose page is outside the pool, whose position is negative or at or behind
  * max_pages * page_size, and rows at or behind cuq[nseq] are not written. No page may receive
- * rows of two sequences in one call.
+ * rows, or a block's sum, of two sequences in one call.
  */
 int moba_cache_append(const moba_paged_cache* cache, const void* k, long long k_stride,
                       const void* v, long long v_stride, const int32_t* cu_seqlens_q_dev, int Tq,
