@@ -270,8 +270,11 @@ typedef struct {
  *   >= 2^-126 that keeps its largest magnitude within 448.
  *   block_sums (when given): blocks that begin with a new row are set to the sum of their new
  *   keys, a block that was begun before is added to. Column sums in a fixed order, fp32. A sequence
- *   that is cut back into a block (rejected draft tokens) leaves their keys in that block's sum:
- *   write the block again from its first row before its sum is used.
+ *   that is cut back into a block (rejected draft tokens) leaves their keys in that block's sum. To
+ *   take draft rows back: before they are written, keep the row of block_sums of the block that the
+ *   sequence ends in (where it ends inside one); afterwards put it back, set seq_lens to the rows
+ *   before plus the accepted ones and write the accepted rows again. Pages and sums are then those of
+ *   a cache that only had the accepted rows, bit for bit.
  * Rows whose page is outside the pool, whose position is negative or at or behind
  * max_pages * page_size, and rows at or behind cuq[nseq] are not written. No page may receive
  * rows, or a block's sum, of two sequences in one call.
