@@ -22,8 +22,8 @@
 // (6.7 TB/s); a ragged batch of 32 with 0.69 GB, 110 us (6.2 TB/s); 1000 tokens, 9 us (latency).
 //
 // e4m3 caches: codes widen exactly to f16, products run in f16 with fp32 accumulation. q is bf16
-// and becomes f16 exactly after a power-of-two scaling of its row (elements 2^-25 below the row's
-// largest round to zero); a key's scale multiplies its logit z in fp32. A value's scale 2^e goes
+// and becomes f16 after a power-of-two scaling of its row (exactly for elements down to 2^-30 of the
+// row's largest; those below 2^-39 of it become zero); a key's scale multiplies its logit z in fp32. A value's scale 2^e goes
 // into the weight: w = 2^(z + e - max(z + e) + 15), so that whatever the scales of a sequence are,
 // the terms that matter most to a sum are the normal f16 numbers up to 2^15 and terms below 2^-29 of
 // them lose digits, while the sum of the weights keeps a maximum of its own (per lane, joined at
@@ -54,6 +54,11 @@ namespace {
 __host__ __device__ constexpr int paged_warps(bool fp8) { return fp8 ? 8 : 4; }
 __host__ __device__ constexpr int tile_bytes(bool fp8) { return fp8 ? 4096 : 8192; }
 constexpr int kStages = 3;
+// CTAs of a cluster that joins a segment, at most: its warps' partials are one to a lane there.
+__host__ __device__ constexpr int join_most(bool fp8) { return fp8 ? 2 : 8; }
+static_assert(join_most(false) * paged_warps(false) <= 32 &&
+                  join_most(true) * paged_warps(true) <= 32,
+              "a cluster's partials are more than the lanes of a warp");
 constexpr int kNoLimit = 0x7fffffff;
 
 // ------------------------------------------------------------------------------ PTX wrappers
@@ -828,7 +833,7 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
   const int mine = (nrow - crank + A.join - 1) / A.join;  // rows of this CTA
   int nr = 1;  // rows at once
   while (nr < mine && nr < kPagedWarps) nr *= 2;
-  const int parts = A.join * kPagedWarps;  // at most 64, two to a lane
+  const int parts = A.join * kPagedWarps;  // at most 32
   const int nslice = kPagedWarps / nr, each = parts / nslice, slice = warp / nr;
   for (int k0 = 0; k0 < mine; k0 += nr) {  // uniform over the CTA
     const int k = k0 + warp % nr, row = crank + k * A.join;
@@ -836,29 +841,18 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
     auto part = [&](int i) {  // partial i in the memory of its CTA
       return cluster.map_shared_rank(smem + (i / A.join) * TL::kWarpBytes, i % A.join);
     };
-    float pm[2], pl[2], top = -INFINITY, sum = 0.f, o[PER];
-    bool nan = over;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      pm[h] = -INFINITY;
-      pl[h] = 0.f;
-      if (on && h * 32 + lane < parts) {
-        const float2 ml =
-            reinterpret_cast<const float2*>(part(h * 32 + lane) + kRows * D * 4)[row];
-        pm[h] = ml.x;
-        pl[h] = ml.y;
-      }
-      nan |= !(pm[h] <= FLT_MAX);
-      top = fmaxf(top, pm[h]);
+    float pm = -INFINITY, pl = 0.f, o[PER];  // partial `lane`
+    if (on && lane < parts) {
+      const float2 ml = reinterpret_cast<const float2*>(part(lane) + kRows * D * 4)[row];
+      pm = ml.x;
+      pl = ml.y;
     }
-    nan = __any_sync(0xffffffffu, nan);
+    bool nan = __any_sync(0xffffffffu, over || !(pm <= FLT_MAX));
+    float top = pm;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      pl[h] = pl[h] > 0.f ? pl[h] * ex2(pm[h] - top) : 0.f;
-      sum += pl[h];
-    }
+    pl = pl > 0.f ? pl * ex2(pm - top) : 0.f;
+    float sum = pl;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
     // a row with a position and without a sum: logits of -inf alone
@@ -870,9 +864,8 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int at = min(i0 + i, parts - 1);
-        const float w0 = __shfl_sync(0xffffffffu, pl[0], at & 31);
-        const float w1 = __shfl_sync(0xffffffffu, pl[1], at & 31);
-        w[i] = i0 + i >= (slice + 1) * each ? 0.f : at < 32 ? w0 : w1;
+        const float wi = __shfl_sync(0xffffffffu, pl, at);
+        w[i] = i0 + i >= (slice + 1) * each ? 0.f : wi;
         const float* src = reinterpret_cast<const float*>(part(at)) + row * D + lane * PER;
 #pragma unroll
         for (int e = 0; e < PER; ++e) v[i][e] = on ? src[e] : 0.f;
@@ -1631,7 +1624,7 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
   // At once means 16 clusters of 8, 32 of 4 or 72 of 2 (a cluster lies within one of the GPU's
   // groups of 18 or 20 SMs): 18 clusters of 8 took 27 us where 9 take 14.
   if (S.nseg <= sms) {
-    const int most = P.fp8 ? 2 : 8;
+    const int most = join_most(P.fp8);
     const double margin = P.fp8 ? 0.75 : 3.0;
     auto at_once = [](int c) { return c == 2 ? 72 : c == 4 ? 32 : 16; };
     int cs = 1;
