@@ -28,8 +28,13 @@
 // the terms that matter most to a sum are the normal f16 numbers up to 2^15 and terms below 2^-29 of
 // them lose digits, while the sum of the weights keeps a maximum of its own (per lane, joined at
 // the segment's end).
-// Rounding: weights to bf16 (e4m3 cache: f16) for the second product; logits, maxima, sums (of the
-// unrounded weights) and outputs are fp32 until the final bf16.
+// Rounding: a bf16 cache's weights enter the second product as two bf16 numbers, the second what the
+// first's rounding left, so that 2^-16 of a weight is lost and not 2^-8 (a decode over a packed cache
+// keeps fp32 weights; the values' bf16 fixes the tensor cores' other operand). The second product of
+// each tile costs 0-1 % where a segment has 8 rows or fewer, 4 % at 16 (8 x up to 20K tokens, 4 rows:
+// 55.7 -> 58.0 us). An e4m3 cache's weights are f16, off by 2^-11 at most, beside codes that were
+// rounded by 2^-4: there a second product would add to the instructions that bound the kernel.
+// Logits, maxima, sums (of the unrounded weights) and outputs are fp32 until the final bf16.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -699,6 +704,7 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
       float corr[NT][2];
       bool grew = false;
       uint32_t pf[MT][NT][2];  // P^T as the second operand: 8 x 8 pieces turned within the warp
+      uint32_t pl[FP8 ? 1 : MT][NT][2];  // bf16: what its rounding leaves
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float w[MT][4];
@@ -758,9 +764,14 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            pf[mt][nt][x] = transpose8x8(FP8 ? pack_f16(w[mt][2 * x], w[mt][2 * x + 1])
-                                             : pack_bf16(w[mt][2 * x], w[mt][2 * x + 1]));
+          for (int x = 0; x < 2; ++x) {
+            const float w0 = w[mt][2 * x], w1 = w[mt][2 * x + 1];
+            const uint32_t high = FP8 ? pack_f16(w0, w1) : pack_bf16(w0, w1);
+            pf[mt][nt][x] = transpose8x8(high);
+            if constexpr (!FP8)
+              pl[mt][nt][x] = transpose8x8(pack_bf16(w0 - __uint_as_float(high << 16),
+                                                     w1 - __uint_as_float(high & 0xffff0000u)));
+          }
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -773,15 +784,26 @@ __global__ void __launch_bounds__(Tile<D, FP8>::kThreads, 1) paged_attn_kernel(c
       // O^T += V^T P^T
       if (!FP8) {
         const int vrow = sub * SUB + ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+        // four accumulators in turn: a product waits for the one four before it
 #pragma unroll
-        for (int ds = 0; ds < KS; ++ds)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t a[4];
-            ldsm4t(a, vb + swz<RB>(vrow + mt * 16, ds * 2 + half));
+          for (int d0 = 0; d0 < KS; d0 += 4) {
+            uint32_t a[4][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              ldsm4t(a[x], vb + swz<RB>(vrow + mt * 16, (d0 + x) * 2 + half));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816<false>(acc[ds][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mma16816<false>(acc[d0 + x][nt], a[x], pf[mt][nt][0], pf[mt][nt][1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mma16816<false>(acc[d0 + x][nt], a[x], pl[FP8 ? 0 : mt][nt][0],
+                                pl[FP8 ? 0 : mt][nt][1]);
           }
       } else {
         // matrices: (keys 0-7, 16 columns), (keys 8-15, same), then the next 16 columns; a

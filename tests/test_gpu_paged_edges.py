@@ -116,3 +116,30 @@ def test_calls_without_the_native_binding(moba, monkeypatch):  # noqa: F811
     want = run()
     monkeypatch.setattr(moba, "_bind", None)
     assert all(torch.equal(a, b) for a, b in zip(run(), want))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_of_bf16_caches_keep_their_digits(moba, d):  # noqa: F811
+    """Values whose weighted sum nearly vanishes, so that a weight's rounding shows: the weights enter
+    the value product as two bf16 numbers, the second the first's rounding error (2^-8 of the weight)
+    rounded again, which leaves 2^-16 of the weight."""
+    lens, h = [2, 3, 5, 9, 17, 40, 700], 4
+    S = Setup(moba, lens, h, d, 16, "bf16")
+    g = _gen(23)
+    T, cu = sum(lens), _cu(lens)
+    k = torch.randn((T, h, d), generator=g, device="cuda").bfloat16()
+    v = torch.randn((T, h, d), generator=g, device="cuda").bfloat16()
+    q = torch.randn((len(lens), h, d), generator=g, device="cuda").bfloat16()
+    for s, (a, b) in enumerate(zip(cu, cu[1:])):
+        z = torch.einsum("uhd,hd->uh", k[a:b].double(), q[s].double()) * d ** -0.5
+        p = torch.softmax(z, 0)
+        top = p.argmax(0)  # the heaviest key's value cancels the others
+        for x in range(h):
+            u = a + int(top[x])
+            rest = (p[:, x, None] * v[a:b, x].double()).sum(0) - p[top[x], x] * v[u, x].double()
+            v[u, x] = (-rest / p[top[x], x]).bfloat16()
+    moba.moba_cache_append(S.cache, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    o, lse = moba.moba_paged_attn_fwd(S.cache, q)
+    rows = [S.rows(s, n) for s, n in enumerate(lens)]
+    want = cref.cached_attention(q, [x[0] for x in rows], [x[1] for x in rows], lens, 1, d ** -0.5)
+    _close(o, lse, want, 2.0 ** -16)
