@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_attn_kernel(
     float ls = 0.f;
 #pragma unroll
     for (int w = 0; w < kDecodeThreads / 32; ++w) ls += red[w];
-    dst[0] = m;   // log2-domain max of the scaled logits
+    // log2-domain max of the scaled logits; fmaxf passes over a NaN among them, the sum keeps it
+    dst[0] = ls == ls ? m : __int_as_float(0x7fffffff);
     dst[1] = ls;  // sum of 2^(z - m)
   }
 }
@@ -304,7 +305,13 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const float* __restri
   if (rh >= Tq * H) return;
   const float* p = part + static_cast<size_t>(rh) * nparts * (D + 2);
   float M = -INFINITY;
-  for (int x = lane; x < nparts; x += 32) M = fmaxf(M, p[static_cast<size_t>(x) * (D + 2)]);
+  bool nan = false;
+  for (int x = lane; x < nparts; x += 32) {
+    const float mx = p[static_cast<size_t>(x) * (D + 2)];
+    nan |= mx != mx;
+    M = fmaxf(M, mx);
+  }
+  nan = __any_sync(0xffffffffu, nan);
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
   constexpr int PER = D / 32;
@@ -324,13 +331,13 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const float* __restri
     }
   }
   const int r = rh / H, h = rh % H;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = nan ? __int_as_float(0x7fffffff) : L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e)
     o[static_cast<size_t>(rh) * D + lane * PER + e] = __float2bfloat16_rn(acc[e] * inv);
   if (lane == 0)
     lse[static_cast<size_t>(h) * Tq + r] =
-        L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+        nan ? inv : L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
 int decode_parts(int B, int topk) { return topk * ((B + kDecodeChunk - 1) / kDecodeChunk); }

@@ -170,6 +170,7 @@ int moba_attn_fwd_kconv(const void* q, const void* k, const void* v, const float
  *                moba_attn_fwd's; centroids may then be NULL).
  * block_idx_out: nullable [Hq, Tq, topk], receives the routing used.
  * o: bf16 [Tq, Hq, d]; lse: fp32 [Hq, Tq] (a sequence with no cached key gives o = 0, lse = -inf).
+ *   A query row that is not finite gives NaN in that row's o and lse.
  * workspace: at least moba_decode_workspace_bytes(...) bytes, 256-byte aligned.
  * The path is HBM-bound: each (row, head) reads the K and V rows of its selected blocks once.
  */
