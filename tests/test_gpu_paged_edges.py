@@ -143,3 +143,35 @@ def test_weights_of_bf16_caches_keep_their_digits(moba, d):  # noqa: F811
     rows = [S.rows(s, n) for s, n in enumerate(lens)]
     want = cref.cached_attention(q, [x[0] for x in rows], [x[1] for x in rows], lens, 1, d ** -0.5)
     _close(o, lse, want, 2.0 ** -16)
+
+
+@pytest.mark.parametrize("topk", [0, 3])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,rows,width", [([1000], 1, 2048), ([5, 300, 0, 64], 2, 5000),
+                                             ([2500] * 9, 1, 600), ([40, 1], 1, 60000)])
+def test_page_tables_wider_than_the_sequences(moba, lens, rows, width, kv, topk):  # noqa: F811
+    """A table for the longest context that a server allows, short sequences in it: the plan goes by
+    the table's width, the results by the lengths."""
+    hq, hkv, d, page, block = 8, 2, 64, 16, 64 if width < 30000 else 128
+    S = Setup(moba, lens, hkv, d, page, kv, block)
+    wide = torch.full((len(lens), width), -1, dtype=torch.int32, device="cuda")
+    wide[:, :S.table.shape[1]] = S.table
+    S.table = wide
+    S.cache = moba.PagedCache(S.k, S.v, wide, S.lens, S.ks, S.vs, S.sums, block)
+    _fill(S, lens)
+    n = len(lens) * rows
+    q = torch.randn((n, hq, d), generator=_gen(9), device="cuda").bfloat16()
+    idx = None
+    if topk:
+        idx = torch.empty((hq, n, topk), dtype=torch.int32, device="cuda")
+        o, lse = moba.moba_paged_decode_fwd(S.cache, q, topk, rows_per_seq=rows, block_idx_out=idx)
+    else:
+        o, lse = moba.moba_paged_attn_fwd(S.cache, q, rows_per_seq=rows)
+    kv_rows = [S.rows(s, x) for s, x in enumerate(lens)]
+    sums = [cref.f64(S.sums[S.table[s, :-(-x // page):block // page].long()])
+            for s, x in enumerate(lens)] if topk else None
+    want = cref.cached_attention(q, [x[0] for x in kv_rows], [x[1] for x in kv_rows], lens, rows,
+                                 d ** -0.5, sums, block, topk)
+    if topk:
+        assert np.array_equal(idx.cpu().numpy(), want[2])
+    _close(o, lse, want, _w(kv))
