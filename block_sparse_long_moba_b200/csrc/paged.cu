@@ -1627,10 +1627,12 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
     S.ent_cap = static_cast<int>(std::min<long long>(
         S.nb_cap, static_cast<long long>(std::min(R, S.rows_per_tile)) * topk));
     S.gate_ctas = 1;
-    // A CTA scores 32 blocks at a time. More CTAs per segment while they all run at once (two fit
-    // an SM); keys and marks of a single CTA stay in its shared memory where they fit.
+    // A CTA scores 32 blocks at a time. More CTAs per segment while they nearly all run at once: two
+    // fit an SM, 30 clusters of 8 the measured GPU (1024 blocks, 31 or 32 segments: one row 24-26 us of
+    // a call with 8 CTAs, 22 with 4, 4 rows 45 : 43, 16 rows 113 : 119). Keys and marks of a single
+    // CTA stay in its shared memory where they fit.
     while (S.gate_ctas < 8 && S.nb_cap > 64 * S.gate_ctas &&
-           S.nseg * S.gate_ctas * 2 <= 256)  // 32 clusters of 8, 64 of 4
+           S.nseg * S.gate_ctas * 2 <= 256)  // up to 32 clusters of 8, 64 of 4
       S.gate_ctas *= 2;
     seg_tiles = std::min(seg_tiles, static_cast<long long>(S.ent_cap) * ((P.B + kt - 1) / kt));
     S.gate_global = S.gate_ctas > 1 ||
@@ -1641,14 +1643,23 @@ PagedShape paged_shape(const PagedCache& P, int rows, int Hq, int topk, int sms)
   // than with the tiles spread over every SM: a bf16 tile takes a warp about 1 us, the merge kernel
   // 3; e4m3 tiles take longer and their 8 warps make more partials, so its margin is smaller and its
   // clusters at most two. Measured, d = 128, 32 / 8 heads, joined against spread and merged:
-  // 16 x 500 tokens 10 us : 15 (either type), 1 x 4000 bf16 11.8 : 13.0, 1 x 8000 bf16 (4.4 tiles
-  // more per warp) 15.2 : 15.0, 4 x 1000 e4m3 (1.1 more) 12.4 : 11.8.
-  // At once means 16 clusters of 8, 32 of 4 or 72 of 2 (a cluster lies within one of the GPU's
-  // groups of 18 or 20 SMs): 18 clusters of 8 took 27 us where 9 take 14.
+  // 16 x 500 tokens 10.4 us : 16 (either type), 1 x 4000 bf16 12.3 : 12.9, 1 x 8000 bf16 (4.4 tiles
+  // more per warp) 16.1 : 14.9, 4 x 1000 e4m3 (1.1 more) 12.5 : 12.0.
+  // At once means 14 clusters of 8, 32 of 4 or 72 of 2: a cluster lies within one of the GPU's groups
+  // of SMs, whose sizes vary; the measured GPU runs 15, 33 and 74, and one cluster more waits for a
+  // whole other to end (2100 tokens, 15 segments joined by 8 CTAs each 11.1 us, 16 segments 20.7, 16
+  // spread and merged 12.1).
+  // Over 1-64 sequences of 100-16000 tokens, 32 / 8, 8 / 1 and 4 / 1 heads of 128, 16 / 16 and 8 / 2 of
+  // 64 (one row a sequence, tables as wide as the sequences) the path taken is within 5 % of the
+  // better of the two in 302 of 336 cases over bf16 caches and in 269 of 336 over e4m3. The worst are
+  // 15 x 2000 bf16 at 32 / 8 heads, 29.8 us spread where a join takes 25.0, and 15 x 1000 e4m3,
+  // 19.2 : 13.1; e4m3 sequences of 250 (d = 64: 500) tokens take 10.6 us where a join takes 8.7.
+  // The plan takes the table's width for the lengths: short sequences behind a wide table are spread
+  // and merged.
   if (S.nseg <= sms) {
     const int most = join_most(P.fp8);
     const double margin = P.fp8 ? 0.75 : 3.0;
-    auto at_once = [](int c) { return c == 2 ? 72 : c == 4 ? 32 : 16; };
+    auto at_once = [](int c) { return c == 2 ? 72 : c == 4 ? 32 : 14; };
     int cs = 1;
     while (cs < most && S.nseg <= at_once(2 * cs) &&
            seg_tiles > static_cast<long long>(cs) * warps)
