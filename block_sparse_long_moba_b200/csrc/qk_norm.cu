@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) qk_norm_rope_kernel(const Nor
   }
 }
 
-// The same for ONE of q and k with fewer heads than a chunk has rows: a chunk is then consecutive
+// The same for ONE of q and k with few heads for the rows of a chunk: a chunk is then consecutive
 // (token, head) rows across tokens, so that it stays full, and every row has an angle of its own.
 // Those come straight from the table into registers one unit ahead (their positions two ahead).
 struct RowsArgs {
@@ -604,12 +604,21 @@ NormArgs args_of(const NormLaunch& L) {
   return A;
 }
 
-// Where a tensor's heads leave chunks partly empty and there are tokens enough that a second launch
-// does not matter, its rows go through the kernel that packs them. Measured by tokens : by rows, heads
-// of 128: 51739 tokens of 4 / 1 heads 57 : 36 us (floor 21), gradients 99 : 57 (31); 16 / 2 heads
-// 93 : 83 (74), gradients 144 : 123 (110); 5000 tokens of 4 / 1 heads 5.8 : 7.0, gradients 17 : 12.
+// Where a tensor's heads leave chunks half empty or more and there are tokens enough that a second
+// launch does not matter, its rows go through the kernel that packs them, whose angles cost more per
+// row. Measured by tokens : by rows (graph replays, us; the tokens that the rule begins at and 65536):
+//   H / H heads of 128 (8 to a chunk)   forward 16384, 65536        gradients 4096, 65536
+//     1 / 1                             18.6 :  6.9,  68.6 :  18.1  11.9 :  8.1, 113.0 :  31.2
+//     2 / 2                             18.4 : 10.7,  68.9 :  36.9  11.9 :  9.1, 112.7 :  61.0
+//     4 / 4 (the last by rows)          18.7 : 17.9,  70.9 :  66.4  12.0 : 13.0, 115.3 : 112.3
+//     5 / 5                             19.6 : 19.3,  75.2 :  79.2  12.2 : 15.7, 117.7 : 137.6
+//     7 / 7                             21.2 : 27.7,  80.0 : 109.5  12.3 : 18.3, 119.0 : 188.4
+//     9 / 9 (two chunks)                39.4 : 39.5, 149.8 : 137.8  19.4 : 18.9, 232.1 : 234.4
+// Heads of 64 (16 to a chunk) alike: 8 / 8 forward 70.2 : 65.4, 9 / 9 74.2 : 70.2, 10 / 10 74.3 : 77.6.
+// With 4 / 1 heads of 128 the two meet at 4096 tokens forward (5.9 : 5.9) and below 2000 in the
+// gradients; 4 / 4 meet at 10000 and 8192.
 bool packed(int H, int d, int T, bool bwd) {
-  return H < chunk_rows(d) && T >= (bwd ? 4096 : 16384);
+  return 2 * H <= chunk_rows(d) && T >= (bwd ? 4096 : 16384);
 }
 int chunks_of(int H, int d) { return (H + chunk_rows(d) - 1) / chunk_rows(d); }
 

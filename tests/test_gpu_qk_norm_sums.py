@@ -31,6 +31,8 @@ CASES = [  # T, hq, hkv, d, rot, interleaved, fused
     (20001, 1, 3, 128, 64, True, False),
     (17000, 16, 2, 128, 32, False, True),   # q by tokens, k by rows
     (16501, 7, 17, 64, 32, True, True),     # and the other way round
+    (17003, 4, 5, 128, 128, False, True),   # on both sides of the rule, half a chunk's heads
+    (4099, 9, 8, 64, 64, True, False),
     (37, 32, 8, 128, 128, False, False),    # fewer chunks than warps
 ]
 
