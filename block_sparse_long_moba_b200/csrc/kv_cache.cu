@@ -19,8 +19,9 @@
 // row maximum is a 3- or 4-step butterfly. The CTAs of a cluster take consecutive parts of the
 // rows and rank 0 adds their column sums in rank order through distributed shared memory: no
 // atomics, the same sum every time. Measured: 101K ragged rows of 8 heads of 128 into e4m3 pages,
-// 0.62 GB, 109 us (5.7 TB/s; about 190 instructions per two rows share the SM with the copies);
-// 64 single rows 3.9 us (latency). Reading them back packed, 1.3 GB: 213 us (6.1 TB/s).
+// 0.62 GB, 109 us in a replayed graph (5.7 TB/s; about 190 instructions per two rows share the SM with
+// the copies), 117 as back-to-back calls; the same rows into bf16 pages, 0.83 GB, 139 us (6.0 TB/s);
+// 64 single rows 4.0 us (latency). Reading e4m3 rows back packed, 1.3 GB: 212 us (6.1 TB/s), 215.
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 

@@ -16,15 +16,16 @@
 // rows), O^T = V^T P^T (16 columns of d x 8 rows). A decode step has 1 to 16 rows per kv head, so
 // the 128-row tile of tcgen05.mma would be 1/8 full at best; here a row tile of 8 wastes at most
 // 7 rows, and the tensor pipe stays far below the memory time: 16 cached bf16 rows of K and V at
-// d = 128 are 8 KB = ~350 clocks of one SM's share of HBM against 16 mma of 16 clocks on each of
-// four tensor units. Bound: HBM, each selected key and value row once. Measured, 32 / 8 heads of
-// 128: 8 x 128K tokens of which the heads of a kv group select 26 of 32 blocks of 4096, 3.6 GB, 535 us
-// (6.7 TB/s); a ragged batch of 32 with 0.69 GB, 110 us (6.2 TB/s); 1000 tokens, 9 us (latency).
+// d = 128 are 8 KB = ~350 clocks of one SM's share of HBM against 24 mma of 16 clocks over four tensor
+// units. Bound: HBM, each selected key and value row once. Measured, 32 / 8 heads of 128, in a replayed
+// graph (and as back-to-back calls): 8 x 128K tokens of which the heads of a kv group select 26 of 32
+// blocks of 4096, 3.6 GB, 528 us (527; 6.8 TB/s); a ragged batch of 32 with 0.69 GB, 113 us (115;
+// 6.1 TB/s); 1000 tokens, 9.3 us (9.8; latency).
 //
 // e4m3 caches: codes widen exactly to f16, products run in f16 with fp32 accumulation. q is bf16
 // and becomes f16 after a power-of-two scaling of its row (exactly for elements down to 2^-30 of the
-// row's largest; those below 2^-39 of it become zero); a key's scale multiplies its logit z in fp32. A value's scale 2^e goes
-// into the weight: w = 2^(z + e - max(z + e) + 15), so that whatever the scales of a sequence are,
+// row's largest; those below 2^-39 of it become zero); a key's scale multiplies its logit z in fp32. A
+// value's scale 2^e goes into the weight: w = 2^(z + e - max(z + e) + 15), so that whatever the scales of a sequence are,
 // the terms that matter most to a sum are the normal f16 numbers up to 2^15 and terms below 2^-29 of
 // them lose digits, while the sum of the weights keeps a maximum of its own (per lane, joined at
 // the segment's end).
@@ -33,8 +34,9 @@
 // keeps fp32 weights; the values' bf16 fixes the tensor cores' other operand). The second product of
 // each tile costs 0-1 % where a segment has 8 rows or fewer, 4 % at 16 (8 x up to 20K tokens, 4 rows:
 // 55.7 -> 58.0 us). An e4m3 cache's weights are f16, off by 2^-11 at most, beside codes that were
-// rounded by 2^-4: there a second product would add to the instructions that bound the kernel.
-// Logits, maxima, sums (of the unrounded weights) and outputs are fp32 until the final bf16.
+// rounded by 2^-4: there a second product costs 6-10 % (8 x 128K tokens 347 -> 369 us, 16 rows a tile
+// 95 -> 104), as instructions bound the kernel, and the error against 64 bits stays that of the bf16
+// output. Logits, maxima, sums (of the unrounded weights) and outputs are fp32 until the final bf16.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -55,7 +57,8 @@ namespace {
 // Warps of a CTA and bytes of K (and of V) per stage: 192 KB of ring either way. An e4m3 tile takes
 // about 930 instructions per 64 keys, a third of them widening codes, so one warp per scheduler
 // cannot keep up with HBM on its dependent steps; two with half the tile can (8 x 128K tokens, 32 / 8
-// heads of 128: 330 us, 6.5 TB/s; 365 us with 4 warps and 8 KB).
+// heads of 128: 328 us in short bursts, 6.6 TB/s, and 347-374 in longer runs under the power cap; 365
+// with 4 warps and 8 KB).
 __host__ __device__ constexpr int paged_warps(bool fp8) { return fp8 ? 8 : 4; }
 __host__ __device__ constexpr int tile_bytes(bool fp8) { return fp8 ? 4096 : 8192; }
 constexpr int kStages = 3;

@@ -14,8 +14,9 @@
 // together. Persistent: every warp takes a chunk of 2 KB (8 or 16 heads of one token) at a time
 // through a private ring in shared memory (16-byte cp.async, with the token's table row).
 // One CTA of 8 warps per SM and two rows at a time: fewer, longer streams suit HBM better than more
-// warps (128K tokens, 32 / 8 heads of 128, 2.7 GB: 407 us = 6.6 TB/s; two CTAs 467, three 465, four
-// rows at a time 440; gradients at 65521 tokens, 16 / 16 heads of 64: 127 us, two CTAs 138).
+// warps (128K tokens, 32 / 8 heads of 128, 2.7 GB: 403-407 us in a replayed graph = 6.7 TB/s, 440 as
+// back-to-back calls on inputs that change; two CTAs 467, three 465, four rows at a time 440; gradients
+// at 65521 tokens, 16 / 16 heads of 64: 121-127 us, back to back 133, two CTAs 138).
 #include <algorithm>
 #include <atomic>
 

@@ -216,7 +216,8 @@ int moba_qk_norm_rope(const void* q, long long q_stride, const void* k, long lon
  *   d_weight = sum over tokens and heads of dz * x r,
  *   dx = r (dz weight - x r mean(dz weight x r)).
  * dq, dk: bf16 [T, Hq, d], [T, Hkv, d], no overlap with q, k (dq may be d_q_out, dk d_k_out);
- * d_q_weight, d_k_weight: fp32 [d] (written, zero when T = 0; the same bits every time).
+ * d_q_weight, d_k_weight: fp32 [d] (written, zero when T = 0; the same bits every time). A token whose
+ * position lies outside the table has NaN gradients, and the weights' are NaN with it.
  * workspace: at least moba_qk_norm_rope_bwd_workspace_bytes(...) bytes, 256-byte aligned.
  */
 size_t moba_qk_norm_rope_bwd_workspace_bytes(int Hq, int Hkv, int d);

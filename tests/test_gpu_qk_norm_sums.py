@@ -65,3 +65,21 @@ def test_no_part_of_a_weight_gradient_is_lost(moba, case):  # noqa: F811
         assert (np.abs(part) > bound).mean() > 0.9
         assert (np.abs(cref.f64(dw) - want) <= bound).all(), float(
             (np.abs(cref.f64(dw) - want) / bound).max())
+
+
+@pytest.mark.parametrize("T", [6, 17003])  # by tokens, by rows
+def test_gradients_of_a_position_outside_the_table(moba, T):  # noqa: F811
+    """NaN in that token's gradients and in the weights', as the forward result was; the other
+    tokens' are right."""
+    q, k, wq, wk, rope, pos = _inputs(moba, T, 4, 2, 128, 64, False, n_pos=50)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    dyq = torch.randn(q.shape, generator=g, device="cuda").bfloat16()
+    dyk = torch.randn(k.shape, generator=g, device="cuda").bfloat16()
+    want = moba.moba_qk_norm_rope_bwd(q, k, wq, wk, rope, pos, dyq, dyk)
+    pos[2], pos[4] = 50, -1
+    got = moba.moba_qk_norm_rope_bwd(q, k, wq, wk, rope, pos, dyq, dyk)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[[2, 4]] = False
+    for a, b in zip(got[:2], want[:2]):
+        assert a[[2, 4]].isnan().all() and torch.equal(a[keep], b[keep])
+    assert got[2].isnan().all() and got[3].isnan().all()

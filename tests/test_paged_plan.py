@@ -16,7 +16,8 @@ def _bytes(lib, nseq, pages, page_size=64, hq=8, hkv=1, topk=0, **kw):  # noqa: 
                                          (18, False)])
 def test_clusters_of_eight_join_only_while_all_run_at_once(lib, nseq, joined):  # noqa: F811
     """4096 tokens in 128 tiles, eight segments or more: a join with eight CTAs to a segment, 4 tiles a
-    warp, is within the margin of 3 of the tiles spread, 1.7 or more; with four CTAs, 8 tiles, it is not. A B200 runs 15 such clusters at once
+    warp, is within the margin of 3 of the tiles spread, 1.7 or more; with four CTAs, 8 tiles, it is
+    not. A B200 runs 15 such clusters at once
     (fewer where its groups of SMs are smaller); a sixteenth would wait for another to end."""
     n = _bytes(lib, nseq, 64)
     assert (n <= 4096) if joined else (n > 1 << 20), n
