@@ -175,3 +175,29 @@ def test_page_tables_wider_than_the_sequences(moba, lens, rows, width, kv, topk)
     if topk:
         assert np.array_equal(idx.cpu().numpy(), want[2])
     _close(o, lse, want, _w(kv))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [40, 700, 20000])
+def test_a_nan_key_is_nan_for_the_rows_that_see_it(moba, n, kv):  # noqa: F811
+    """A token whose key is NaN (its position lay outside the rotary table) as the newest of three:
+    NaN for its own row, nothing to the rows before it; as an older one: NaN for all of them."""
+    hkv, hq, d, rows = 2, 4, 64, 3
+    S = Setup(moba, [n, n], hkv, d, 16, kv)
+    g = _gen(29)
+    k = torch.randn((2 * n, hkv, d), generator=g, device="cuda").bfloat16()
+    v = torch.randn((2 * n, hkv, d), generator=g, device="cuda").bfloat16()
+    clean = k.clone()
+    k[n - 1] = float("nan")          # newest of sequence 0
+    k[n + n // 2, 0] = float("nan")  # one kv head of a token in the middle of sequence 1
+    q = torch.randn((2 * rows, hq, d), generator=g, device="cuda").bfloat16()
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    moba.moba_cache_append(S.cache, clean, v, cu)
+    want = moba.moba_paged_attn_fwd(S.cache, q, rows_per_seq=rows)
+    moba.moba_cache_append(S.cache, k, v, cu)
+    o, lse = moba.moba_paged_attn_fwd(S.cache, q, rows_per_seq=rows)
+    bad = torch.zeros((2 * rows, hq), dtype=torch.bool, device="cuda")
+    bad[rows - 1] = True
+    bad[rows:, :hq // hkv] = True
+    assert o[bad].isnan().all() and lse.T[bad].isnan().all()
+    assert torch.equal(o[~bad], want[0][~bad]) and torch.equal(lse.T[~bad], want[1].T[~bad])
