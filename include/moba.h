@@ -310,7 +310,8 @@ int moba_cache_read(const moba_paged_cache* cache, const int32_t* cu_seqlens_dev
  * sequence is cut over the SMs depends on all lengths of the call, so the last bits of its rows may
  * differ in another batch. Cached values that a row must not see may be anything in rows at
  * or behind seq_lens[s]; cached rows are to be finite, but for a key that is NaN (a token whose
- * position lay outside its table): it gives NaN to the rows that attend it and nothing to the others.
+ * position lay outside its table): it gives NaN to the rows that attend it and nothing to the others
+ * (its block's sum is NaN with it and ranks last).
  * workspace: at least moba_paged_workspace_bytes(...) (topk 0 for moba_paged_attn_fwd; depends on
  * the sizes alone, not on lengths), 256-byte aligned, for one call at a time; it holds nothing
  * between calls.
