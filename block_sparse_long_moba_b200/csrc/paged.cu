@@ -24,11 +24,11 @@
 //
 // e4m3 caches: codes widen exactly to f16, products run in f16 with fp32 accumulation. q is bf16
 // and becomes f16 after a power-of-two scaling of its row (exactly for elements down to 2^-30 of the
-// row's largest; those below 2^-39 of it become zero); a key's scale multiplies its logit z in fp32. A
-// value's scale 2^e goes into the weight: w = 2^(z + e - max(z + e) + 15), so that whatever the scales of a sequence are,
-// the terms that matter most to a sum are the normal f16 numbers up to 2^15 and terms below 2^-29 of
-// them lose digits, while the sum of the weights keeps a maximum of its own (per lane, joined at
-// the segment's end).
+// row's largest; those below 2^-39 of it become zero); a key's scale multiplies its logit z in fp32.
+// A value's scale 2^e goes into the weight: w = 2^(z + e - max(z + e) + 15), so that whatever the
+// scales of a sequence are, the terms that matter most to a sum are the normal f16 numbers up to 2^15
+// and terms below 2^-29 of them lose digits, while the sum of the weights keeps a maximum of its own
+// (per lane, joined at the segment's end).
 // Rounding: a bf16 cache's weights enter the second product as two bf16 numbers, the second what the
 // first's rounding left, so that 2^-16 of a weight is lost and not 2^-8 (a decode over a packed cache
 // keeps fp32 weights; the values' bf16 fixes the tensor cores' other operand). The second product of
